@@ -158,6 +158,76 @@ mg_status mgemm_dgrad_swiglu(const void* dy, const void* w2, const void* gu,
 mg_status mg_moe_combine(const void* rows, const int32_t* token_rows, const float* weights,
                          void* out, int64_t M, int64_t T, int32_t k, int64_t D, void* stream);
 
+/* Gradient of mg_moe_combine with respect to its rows and weights:
+ *   drows[r, :]    = weights[t, j] dout[t, :]          r = token_rows[t, j]
+ *   dweights[t, j] = sum_d rows[r, d] dout[t, d]       (0 where there is no row)
+ * dout: bf16 [T, D]; rows: bf16 [M, D] (read only for dweights; may be NULL
+ * without it); weights: fp32 [T, k] or NULL (all 1); drows: bf16 [M, D]
+ * (written, one rounding; rows that no entry names are left as they were);
+ * dweights: fp32 [T, k] (written) or NULL.  Every row index may occur once in
+ * token_rows, as mg_moe_route makes it (checked only under MGEMM_VALIDATE=1:
+ * of a row named twice one of the two gradients would remain).  fp32
+ * arithmetic, bitwise reproducible.  D a multiple of 8, 1 <= k <= 64; dout,
+ * rows and drows 16-byte aligned.  T == 0 is a no-op; D == 0 or M == 0 writes
+ * zero dweights.  Allocates nothing. */
+mg_status mg_moe_combine_bwd(const void* dout, const void* rows, const int32_t* token_rows,
+                             const float* weights, void* drows, float* dweights, int64_t M,
+                             int64_t T, int32_t k, int64_t D, void* stream);
+
+/* Router: from logits to the gate, the row order of the grouped products
+ * (offsets and gather of mgemm_fwd_swiglu, token_rows and weights of
+ * mg_moe_combine), and the statistics and losses of the experts' balance.
+ * logits: fp32 (logits_bf16 == 0) or bf16 [T, E]; mask: uint8 [T] or NULL, 0 =
+ * a padding token.  NaN counts as -inf and +inf as the largest finite value;
+ * an expert at -inf is never chosen.  A token that is masked, or has no logit
+ * above -inf, does not count: its experts are -1, its weights and lse 0.
+ *   p[t, e] = exp(logits[t, e] - lse[t]), lse[t] = log sum_e exp(logits[t, e])
+ *   experts[t, j] (int32 [T, k]): the k largest logits, descending, ties to the
+ *     lower index; -1 where fewer than k are above -inf
+ *   weights[t, j] (fp32 [T, k]): p of the chosen, with normalize over their sum
+ *   counts[e] (int32 [E]): entries of experts equal to e
+ *   prob_sum[e] (fp32 [E]) = sum over counting tokens of p[t, e]
+ *   tokens[0] (int32): the number of counting tokens, n
+ *   loss[0] (fp32) = E sum_e (counts[e] / sum counts) (prob_sum[e] / n)
+ *   loss[1] = sum_t lse[t]^2 / n          (both 0 for n == 0)
+ *   offsets (int32 [local + 1]): rows of the experts first .. first + local - 1
+ *   gather (int32 [T k]): the token of each row, rows sorted by (expert,
+ *     token); -1 behind row offsets[local]
+ *   token_rows (int32 [T, k]): the row of entry (t, j), -1 for no expert or one
+ *     outside the local range
+ * All outputs are written whole.  workspace: mg_moe_route_workspace(T, E)
+ * bytes of DEVICE memory (4-byte aligned, no contents expected or kept; 0
+ * bytes for short batches); calls that may run at the same time need one each.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 64), T k < 2^31.  Sums in fp32 in a fixed
+ * order: bitwise reproducible.  T == 0 writes the zero statistics.  Allocates
+ * nothing; at most three kernels. */
+mg_status mg_moe_route(const void* logits, int32_t logits_bf16, const uint8_t* mask, int64_t T,
+                       int32_t E, int32_t k, int32_t normalize, int32_t first, int32_t local,
+                       float* weights, int32_t* experts, float* lse, int32_t* counts,
+                       float* prob_sum, int32_t* tokens, float* loss, int32_t* offsets,
+                       int32_t* gather, int32_t* token_rows, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Bytes of mg_moe_route's workspace (0 for sizes that it refuses). */
+int64_t mg_moe_route_workspace(int64_t T, int32_t E);
+
+/* Gradient of mg_moe_route to the logits, from upstream gradients dweights
+ * (fp32 [T, k], or NULL) of the weights and dloss (fp32 [2], or NULL) of the
+ * two losses; the choice of experts, counts and n are held fixed:
+ *   dlogits[t, e] = p (g_e - sum_f p[t, f] g_f + 2 dloss[1] lse[t] / n) + gate,
+ *   g_e = dloss[0] E counts[e] / (n sum counts),
+ *   gate = w_j (dw_j - sum_i w_i dw_i) at the chosen (normalize), or
+ *          w_j dw_j at the chosen - p sum_i w_i dw_i.
+ * weights, experts, lse: the forward's.  counts (int32 [E]) and tokens (int32
+ * [1]): the forward's, or their sums over ranks for a balance over all ranks'
+ * tokens (needed only with dloss).  dlogits: [T, E] in the logits' type
+ * (written whole; zeros for tokens that do not count).  Allocates nothing. */
+mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float* weights,
+                           const int32_t* experts, const float* lse, const int32_t* counts,
+                           const int32_t* tokens, const float* dweights, const float* dloss,
+                           void* dlogits, int64_t T, int32_t E, int32_t k, int32_t normalize,
+                           void* stream);
+
 /* One group of mgemm_list: D [m, n] = A [m, k] B [n, k]^T (bf16 in and out,
  * fp32 accumulation, round to nearest even), row-major with row strides in
  * elements.  All three pointers are DEVICE pointers, 16-byte aligned; k, n and
@@ -268,6 +338,72 @@ mg_status kgemm_wgrad_mx_tm(const void* dy8, const void* dy_scale, const void* x
 mg_status mg_mx_scales_blocked(const void* scales, void* blocked, int64_t rows, int64_t K,
                                int64_t batch, void* stream);
 
+/* Values to block-scaled fp8 rows, the activations of the products below
+ * (quantization along the reduction axis, DeepGEMM issue #10):
+ *   a = max(max |x| over a row's 128 columns, 2^-100), scale = a / 448,
+ *   code = e4m3(x (448 / a))   (round to nearest even; fp32 arithmetic)
+ * x: bf16 (x_fp32 == 0) or fp32 [M, K], or with gather != NULL [T, K], row i
+ * being x[gather[i]] (int32 DEVICE array [M]; an index outside [0, T) reads
+ * zeros); codes: uint8 E4M3 [M, K] (written); scales: fp32 [ceil(K/128), M]
+ * (written).  offsets: NULL, or the int32 DEVICE array [E + 1] of the grouped
+ * rows: rows i >= offsets[E] of codes and scales are then left as they were.
+ * A NaN or infinity makes NaN codes in its block.  K a multiple of 16; x and
+ * codes 16-byte aligned.  M == 0 or K == 0 is a no-op.  Allocates nothing. */
+mg_status mg_fp8_quantize(const void* x, int32_t x_fp32, const int32_t* gather,
+                          const int32_t* offsets, void* codes, float* scales, int64_t M, int64_t T,
+                          int64_t K, int32_t E, void* stream);
+
+/* The same of h = silu(g) u, computed in fp32 from gu: bf16 [M, 2I] = g | u
+ * (the gate-up product): codes [M, I], scales [ceil(I/128), M]; I a multiple
+ * of 16. */
+mg_status mg_fp8_quantize_swiglu(const void* gu, const int32_t* offsets, void* codes, float* scales,
+                                 int64_t M, int64_t I, int32_t E, void* stream);
+
+/* Weights to block-scaled fp8, one scale per 128 x 128 block (of an expert;
+ * edge blocks are smaller), by the rule of mg_fp8_quantize: w: bf16 or fp32
+ * [E, N, K]; codes: uint8 [E, N, K]; scales: fp32 [E, ceil(N/128),
+ * ceil(K/128)].  K a multiple of 16.  Empty sizes are a no-op.  Allocates
+ * nothing. */
+mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, float* scales,
+                                  int64_t E, int64_t N, int64_t K, void* stream);
+
+/* Block-scaled fp8 M-grouped forward: E4M3 elements, one fp32 scale per row
+ * and 128 consecutive reduction steps of x, one per 128 x 128 block of w
+ * (the block scaling of the fp8 grouped GEMMs of DeepGEMM issue #10):
+ *   y[i, n] = sum_k X[i, k] W[e, n, k]   for offsets[e] <= i < offsets[e+1],
+ *   X[i, k] = e4m3(x8[i, k]) x_scale[k / 128, i],
+ *   W[e, n, k] = e4m3(w8[e, n, k]) w_scale[e, n / 128, k / 128].
+ * x8: uint8 E4M3 codes [M, K]; x_scale: fp32 [ceil(K/128), M]; w8: uint8
+ * [E, N, K]; w_scale: fp32 [E, ceil(N/128), ceil(K/128)]; y: bf16 [M, N]
+ * (written, round to nearest even).  mg_fp8_quantize and
+ * mg_fp8_quantize_weights make these operands.  A scale may be any fp32 value;
+ * a NaN code or scale makes NaN in the outputs that it enters and no others.
+ * Each block's 128 products are summed by the fp8 matrix-core instruction
+ * (measured exact to 1.5e-5 of a block's sum for normally distributed values),
+ * the blocks by fp32 fmas in ascending order, or, for few rows per expert, in
+ * four such sums added in a fixed order: results are bitwise reproducible.
+ * N and K multiples of 16.  x8, w8, y 16-byte aligned, scales 4-byte aligned.
+ * Rows i >= offsets[E] of y are not touched.  M == 0 or N == 0 is a no-op;
+ * K == 0 writes zeros.  Allocates nothing.  max_m_per_e: launch-size hint, as
+ * for mgemm_fwd (which variant runs, and so the order of the sums, may
+ * depend on it). */
+mg_status mgemm_fwd_fp8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
+                        const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int32_t E,
+                        int64_t max_m_per_e, void* stream);
+
+/* Block-scaled fp8 M-grouped input gradient, on the forward's weights as they
+ * are stored (the 128 x 128 blocks' scales serve both directions):
+ *   dx[i, k] = sum_n DY[i, n] W[e, n, k]   for offsets[e] <= i < offsets[e+1],
+ *   DY[i, n] = e4m3(dy8[i, n]) dy_scale[n / 128, i],  W as for mgemm_fwd_fp8.
+ * dy8: uint8 E4M3 codes [M, N]; dy_scale: fp32 [ceil(N/128), M]; dx: bf16
+ * [M, K] (written).  Otherwise as mgemm_fwd_fp8.  M == 0 or K == 0 is a no-op;
+ * N == 0 writes zeros.  The weight gradient of the same layer is kgemm_wgrad
+ * on the bf16 rows: the fp8 products would cost its fp32 sums about 7 of
+ * their 24 bits. */
+mg_status mgemm_dgrad_fp8(const void* dy8, const float* dy_scale, const void* w8,
+                          const float* w_scale, const int32_t* offsets, void* dx, int64_t M,
+                          int64_t N, int64_t K, int32_t E, int64_t max_m_per_e, void* stream);
+
 /* K-grouped weight gradient in FP32 (RapidGEMM README, "Kernels", Kgemm;
  * wgrad is x^T dy, DeepGEMM issue #10, laid out like w so it can update w):
  *   dw[e, n, k] (= or +=) sum_{offsets[e] <= i < offsets[e+1]} dy[i, n] * x[i, k]
@@ -321,6 +457,10 @@ int32_t mg_abi_version(void);
  * MG_OK if offsets[0] == 0, non-decreasing, offsets[E] <= M; MG_ERR_OFFSETS
  * otherwise; MG_ERR_NULL / MG_ERR_SHAPE for a NULL pointer or bad E / M. */
 mg_status mg_check_offsets_host(const int32_t* offsets_host, int32_t E, int64_t M);
+
+/* Host-side check of n entries of a token-to-row table held in HOST memory:
+ * MG_OK if no index in [0, M) occurs twice, else MG_ERR_OFFSETS. */
+mg_status mg_check_rows_host(const int32_t* token_rows_host, int64_t n, int64_t M);
 
 #ifdef __cplusplus
 }

@@ -16,18 +16,26 @@ Page-shaped aliases follow the RapidGEMM README ("Kernels"):
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
 from ._lib import LIB, GemmDesc, MgemmError, check, status_str  # noqa: F401
 
 __all__ = ["fwd", "dgrad", "wgrad", "wgrad_noalloc", "fwd_swiglu", "dgrad_swiglu",
            "moe_combine", "grouped_list", "list_descriptors", "grouped_list_desc",
-           "mx_scales_blocked", "fwd_mx", "wgrad_mx", "wgrad_mx_tm", "Mgemm", "Kgemm",
+           "mx_scales_blocked", "fwd_mx", "wgrad_mx", "wgrad_mx_tm", "fp8_quantize", "fp8_quantize_swiglu",
+           "fp8_quantize_weights", "fwd_fp8", "dgrad_fp8", "Route", "moe_route", "moe_route_bwd",
+           "moe_combine_bwd", "Mgemm", "Kgemm",
            "MgemmError", "status_str", "LIB"]
 
 
 def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _ptr(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
@@ -362,6 +370,164 @@ def fwd_mx(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scale: t
     return out
 
 
+def _codes_out(M, K, dev, out, scales, shape):
+    nb = (K + 127) // 128
+    if out is None:
+        out = torch.empty(shape + (K,), dtype=torch.uint8, device=dev)
+    else:
+        _need(out, "out", torch.uint8, len(shape) + 1)
+        if tuple(out.shape) != shape + (K,):
+            raise ValueError(f"out must be {list(shape + (K,))}")
+    if scales is None:
+        scales = torch.empty((nb, M), dtype=torch.float32, device=dev)
+    else:
+        _need(scales, "scales", torch.float32, 2)
+        if tuple(scales.shape) != (nb, M):
+            raise ValueError(f"scales must be [{nb}, {M}]")
+    return out, scales
+
+
+def _rows_offsets(offsets, dev):
+    if offsets is None:
+        return 0
+    _need(offsets, "offsets", torch.int32, 1)
+    if offsets.numel() < 2:
+        raise ValueError("offsets must have E+1 entries")
+    _same_device(dev, offsets=offsets)
+    return offsets.numel() - 1
+
+
+def fp8_quantize(x: torch.Tensor, gather: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None):
+    """Rows to block-scaled fp8: (uint8 E4M3 codes [M, K], fp32 scales [ceil(K/128), M]).
+
+    x bf16 or fp32 [M, K]; each row's 128 columns get the scale max|x| / 448.
+    With `gather` (int32 [M]) row i is x[gather[i]] of x [T, K] (an index
+    outside [0, T) gives zeros).  With `offsets` (int32 [E+1]) rows past
+    offsets[E] are left untouched.  K a multiple of 16."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    _need(x, "x", x.dtype, 2)
+    T, K = x.shape
+    M = T
+    if gather is not None:
+        _need(gather, "gather", torch.int32, 1)
+        _same_device(x.device, gather=gather)
+        M = gather.numel()
+    E = _rows_offsets(offsets, x.device)
+    out, scales = _codes_out(M, K, x.device, out, scales, (M,))
+    _same_device(x.device, out=out, scales=scales)
+    with torch.cuda.device(x.device):
+        st = LIB.mg_fp8_quantize(x.data_ptr(), 1 if x.dtype == torch.float32 else 0, _ptr(gather),
+                                 _ptr(offsets), out.data_ptr(), scales.data_ptr(), M, T, K, E,
+                                 _stream(x))
+    check(st, "mg_fp8_quantize")
+    return out, scales
+
+
+def fp8_quantize_swiglu(gu: torch.Tensor, offsets: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """fp8_quantize of silu(g) u, in fp32 from gu = g | u (bf16 [M, 2I]):
+    (codes [M, I], scales [ceil(I/128), M]); I a multiple of 16."""
+    _need(gu, "gu", torch.bfloat16, 2)
+    M, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError(f"gu must hold two halves (2I columns), got {I2}")
+    E = _rows_offsets(offsets, gu.device)
+    out, scales = _codes_out(M, I2 // 2, gu.device, out, scales, (M,))
+    _same_device(gu.device, out=out, scales=scales)
+    with torch.cuda.device(gu.device):
+        st = LIB.mg_fp8_quantize_swiglu(gu.data_ptr(), _ptr(offsets), out.data_ptr(),
+                                        scales.data_ptr(), M, I2 // 2, E, _stream(gu))
+    check(st, "mg_fp8_quantize_swiglu")
+    return out, scales
+
+
+def fp8_quantize_weights(w: torch.Tensor, out: torch.Tensor | None = None,
+                         scales: torch.Tensor | None = None):
+    """Weights (bf16 or fp32 [E, N, K]) to block-scaled fp8: (uint8 codes
+    [E, N, K], fp32 scales [E, ceil(N/128), ceil(K/128)]), one scale per
+    128 x 128 block.  K a multiple of 16."""
+    if not isinstance(w, torch.Tensor) or w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("w must be a torch.bfloat16 or torch.float32 tensor")
+    _need(w, "w", w.dtype, 3)
+    E, N, K = w.shape
+    shape = (E, (N + 127) // 128, (K + 127) // 128)
+    if out is None:
+        out = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
+    else:
+        _need(out, "out", torch.uint8, 3)
+        if tuple(out.shape) != (E, N, K):
+            raise ValueError(f"out must be [{E}, {N}, {K}]")
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=w.device)
+    else:
+        _need(scales, "scales", torch.float32, 3)
+        if tuple(scales.shape) != shape:
+            raise ValueError(f"scales must be {list(shape)}")
+    _same_device(w.device, out=out, scales=scales)
+    with torch.cuda.device(w.device):
+        st = LIB.mg_fp8_quantize_weights(w.data_ptr(), 1 if w.dtype == torch.float32 else 0,
+                                         out.data_ptr(), scales.data_ptr(), E, N, K, _stream(w))
+    check(st, "mg_fp8_quantize_weights")
+    return out, scales
+
+
+def fwd_fp8(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor,
+            offsets: torch.Tensor, max_m_per_e: int = 0,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Block-scaled fp8 M-grouped forward: out[i] = X[i] @ W[e].T.
+
+    x8 uint8 E4M3 codes [M, K] with x_scale fp32 [ceil(K/128), M] (one scale per
+    row and 128 columns, as fp8_quantize returns them), w8 [E, N, K] with
+    w_scale fp32 [E, ceil(N/128), ceil(K/128)] (one per 128 x 128 block, as
+    fp8_quantize_weights returns them); N and K multiples of 16.  out bf16
+    [M, N]; rows past offsets[E] are left untouched."""
+    return _product_fp8("mgemm_fwd_fp8", False, x8, x_scale, w8, w_scale, offsets, max_m_per_e, out)
+
+
+def dgrad_fp8(dy8: torch.Tensor, dy_scale: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor,
+              offsets: torch.Tensor, max_m_per_e: int = 0,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """Block-scaled fp8 M-grouped input gradient: out[i] = DY[i] @ W[e].
+
+    dy8 uint8 E4M3 codes [M, N] with dy_scale fp32 [ceil(N/128), M]; w8 and
+    w_scale as for fwd_fp8.  out bf16 [M, K]."""
+    return _product_fp8("mgemm_dgrad_fp8", True, dy8, dy_scale, w8, w_scale, offsets, max_m_per_e,
+                        out)
+
+
+def _product_fp8(fn, dgrad, q8, q_scale, w8, w_scale, offsets, max_m_per_e, out):
+    q, scale = ("dy8", "dy_scale") if dgrad else ("x8", "x_scale")
+    _need(q8, q, torch.uint8, 2)
+    _need(w8, "w8", torch.uint8, 3)
+    M, R = q8.shape
+    E, N, K = w8.shape
+    if R != (N if dgrad else K):
+        raise ValueError(f"{q} is [M, {R}] but w8 is [E, {N}, {K}]")
+    _need(q_scale, scale, torch.float32, 2)
+    _need(w_scale, "w_scale", torch.float32, 3)
+    nn, nk, nr = (N + 127) // 128, (K + 127) // 128, (R + 127) // 128
+    if tuple(q_scale.shape) != (nr, M) or tuple(w_scale.shape) != (E, nn, nk):
+        raise ValueError(f"scales must be [{nr}, {M}] and [{E}, {nn}, {nk}]")
+    _offsets(offsets, E, q8.device)
+    P = K if dgrad else N
+    if out is None:
+        out = torch.empty((M, P), dtype=torch.bfloat16, device=q8.device)
+    else:
+        _need(out, "out", torch.bfloat16, 2)
+        if tuple(out.shape) != (M, P):
+            raise ValueError(f"out must be [{M}, {P}]")
+    _same_device(q8.device, w8=w8, out=out, **{scale: q_scale, "w_scale": w_scale})
+    with torch.cuda.device(q8.device):
+        st = getattr(LIB, fn)(q8.data_ptr(), q_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
+                              offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e),
+                              _stream(q8))
+    check(st, fn)
+    return out
+
+
 def wgrad_mx(dyt8: torch.Tensor, dyt_scale: torch.Tensor, xt8: torch.Tensor,
              xt_scale: torch.Tensor, offsets: torch.Tensor, E: int | None = None,
              out: torch.Tensor | None = None, accumulate: bool = False) -> torch.Tensor:
@@ -471,6 +637,161 @@ def moe_combine(rows: torch.Tensor, token_rows: torch.Tensor,
         st = LIB.mg_moe_combine(rows.data_ptr(), token_rows.data_ptr(), wptr, out.data_ptr(),
                                 M, T, k, D, _stream(rows))
     check(st, "mg_moe_combine")
+    return out
+
+
+def moe_combine_bwd(dout: torch.Tensor, rows: torch.Tensor, token_rows: torch.Tensor,
+                    weights: torch.Tensor | None = None, drows: torch.Tensor | None = None):
+    """Gradient of moe_combine: (drows bf16 [M, D], dweights fp32 [T, k]).
+
+    drows[token_rows[t, j]] = weights[t, j] dout[t], dweights[t, j] =
+    rows[token_rows[t, j]] . dout[t]; dweights is None without weights.  No row
+    may be named twice by token_rows (moe_route names none twice); rows that
+    none names are left untouched in `drows` (zeros when it is None)."""
+    _need(dout, "dout", torch.bfloat16, 2)
+    _need(rows, "rows", torch.bfloat16, 2)
+    _need(token_rows, "token_rows", torch.int32, 2)
+    M, D = rows.shape
+    T, k = token_rows.shape
+    if tuple(dout.shape) != (T, D):
+        raise ValueError(f"dout must be [{T}, {D}]")
+    dweights = None
+    if weights is not None:
+        _need(weights, "weights", torch.float32, 2)
+        if tuple(weights.shape) != (T, k):
+            raise ValueError(f"weights must be [{T}, {k}]")
+        dweights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    if drows is None:
+        drows = torch.zeros((M, D), dtype=torch.bfloat16, device=rows.device)
+    else:
+        _need(drows, "drows", torch.bfloat16, 2)
+        if tuple(drows.shape) != (M, D):
+            raise ValueError(f"drows must be [{M}, {D}]")
+    _same_device(rows.device, dout=dout, token_rows=token_rows, weights=weights, drows=drows)
+    with torch.cuda.device(rows.device):
+        st = LIB.mg_moe_combine_bwd(dout.data_ptr(), rows.data_ptr(), token_rows.data_ptr(),
+                                    _ptr(weights), drows.data_ptr(), _ptr(dweights), M, T, k, D,
+                                    _stream(rows))
+    check(st, "mg_moe_combine_bwd")
+    return drows, dweights
+
+
+class Route(NamedTuple):
+    """What moe_route computes (sizes for T tokens, E experts, k per token)."""
+    weights: torch.Tensor     # fp32 [T, k]   gate weights (moe_combine's weights)
+    experts: torch.Tensor     # int32 [T, k]  chosen experts, -1 = none
+    lse: torch.Tensor         # fp32 [T]      log-sum-exp of the logits
+    counts: torch.Tensor      # int32 [E]     entries per expert
+    prob_sum: torch.Tensor    # fp32 [E]      sum of the probabilities
+    tokens: torch.Tensor      # int32 [1]     tokens that count
+    loss: torch.Tensor        # fp32 [2]      balance loss, z loss
+    offsets: torch.Tensor     # int32 [local + 1]  row ranges of the local experts
+    gather: torch.Tensor      # int32 [T k]   token of each row, -1 behind the last
+    token_rows: torch.Tensor  # int32 [T, k]  row of each entry, -1 = none
+
+
+def _logits(logits: torch.Tensor) -> None:
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    _need(logits, "logits", logits.dtype, 2)
+
+
+def moe_route(logits: torch.Tensor, k: int, normalize: bool = True,
+              mask: torch.Tensor | None = None, first: int = 0,
+              local: int | None = None) -> Route:
+    """Router: gate, row order and balance of logits [T, E] (fp32 or bf16).
+
+    The k largest logits of a token choose its experts (ties to the lower
+    index); `normalize` divides their softmax probabilities by their sum.
+    `mask` (bool or uint8 [T]) leaves out padding tokens; an expert whose logit
+    is -inf (or NaN) is never chosen.  offsets, gather and token_rows describe
+    the rows of experts first .. first + local - 1 (all by default), as
+    fwd_swiglu, fp8_quantize and moe_combine take them.  loss = (balance, z):
+    E sum_e (counts_e / sum counts) (prob_sum_e / n), and the mean of lse^2."""
+    _logits(logits)
+    T, E = logits.shape
+    k = int(k)
+    if not 1 <= k <= min(E, 64):
+        raise ValueError(f"k must be in [1, min(E, 64)] = [1, {min(E, 64)}], got {k}")
+    local = E - first if local is None else int(local)
+    if first < 0 or local < 1 or first + local > E:
+        raise ValueError(f"experts {first} .. {first + local - 1} are not among {E}")
+    if mask is not None:
+        if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _need(mask, "mask", torch.uint8, 1)
+        if mask.numel() != T:
+            raise ValueError(f"mask must have {T} entries, got {mask.numel()}")
+        _same_device(logits.device, mask=mask)
+    dev = logits.device
+    # one allocation per type: the outputs are slices of it
+    f = torch.empty(T * k + T + E + 2, dtype=torch.float32, device=dev)
+    words = LIB.mg_moe_route_workspace(T, E) // 4
+    i = torch.empty(3 * T * k + E + 1 + local + 1, dtype=torch.int32, device=dev)
+    work = torch.empty(words, dtype=torch.int32, device=dev)
+    weights, lse, prob_sum, loss = f.split([T * k, T, E, 2])
+    experts, gather, token_rows, counts, tokens, offsets = i.split([T * k, T * k, T * k, E, 1,
+                                                                    local + 1])
+    r = Route(weights.view(T, k), experts.view(T, k), lse, counts, prob_sum, tokens, loss, offsets,
+              gather, token_rows.view(T, k))
+    with torch.cuda.device(dev):
+        st = LIB.mg_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
+                              _ptr(mask), T, E, k, 1 if normalize else 0, int(first), local,
+                              r.weights.data_ptr(), r.experts.data_ptr(), r.lse.data_ptr(),
+                              r.counts.data_ptr(), r.prob_sum.data_ptr(), r.tokens.data_ptr(),
+                              r.loss.data_ptr(), r.offsets.data_ptr(), r.gather.data_ptr(),
+                              r.token_rows.data_ptr(), work.data_ptr(), 4 * words,
+                              _stream(logits))
+    check(st, "mg_moe_route")
+    return r
+
+
+def moe_route_bwd(logits: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor,
+                  lse: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                  dweights: torch.Tensor | None = None, dloss: torch.Tensor | None = None,
+                  normalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of moe_route to the logits (their type, [T, E]).
+
+    weights, experts, lse, counts and tokens are the forward's; for a balance
+    over several ranks' tokens, counts and tokens are their sums.  dweights
+    (fp32 [T, k]) is the gradient of the weights, dloss (fp32 [2]) that of
+    (balance, z); either may be None.  `normalize` as in the forward."""
+    _logits(logits)
+    T, E = logits.shape
+    _need(experts, "experts", torch.int32, 2)
+    k = experts.shape[1]
+    if experts.shape[0] != T:
+        raise ValueError(f"experts must be [{T}, k]")
+    for name, t in (("weights", weights), ("dweights", dweights)):
+        if t is not None or name == "weights":
+            _need(t, name, torch.float32, 2)
+            if tuple(t.shape) != (T, k):
+                raise ValueError(f"{name} must be [{T}, {k}]")
+    _need(lse, "lse", torch.float32, 1)
+    _need(counts, "counts", torch.int32, 1)
+    _need(tokens, "tokens", torch.int32, 1)
+    if lse.numel() != T or counts.numel() != E or tokens.numel() != 1:
+        raise ValueError(f"lse, counts and tokens must have {T}, {E} and 1 entries")
+    if dloss is not None:
+        _need(dloss, "dloss", torch.float32, 1)
+        if dloss.numel() != 2:
+            raise ValueError("dloss must have 2 entries (balance, z)")
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _need(out, "out", logits.dtype, 2)
+        if tuple(out.shape) != (T, E):
+            raise ValueError(f"out must be [{T}, {E}]")
+    _same_device(logits.device, weights=weights, experts=experts, lse=lse, counts=counts,
+                 tokens=tokens, dweights=dweights, dloss=dloss, out=out)
+    with torch.cuda.device(logits.device):
+        st = LIB.mg_moe_route_bwd(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
+                                  weights.data_ptr(), experts.data_ptr(), lse.data_ptr(),
+                                  counts.data_ptr(), tokens.data_ptr(), _ptr(dweights), _ptr(dloss),
+                                  out.data_ptr(), T, E, k, 1 if normalize else 0, _stream(logits))
+    check(st, "mg_moe_route_bwd")
     return out
 
 

@@ -30,6 +30,18 @@ SIGNATURES = {
     "mg_mx_scales_blocked": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp]),
     "kgemm_wgrad_mx": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp]),
     "kgemm_wgrad_mx_tm": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "mgemm_fwd_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i64, _vp]),
+    "mgemm_dgrad_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i64, _vp]),
+    "mg_fp8_quantize": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp]),
+    "mg_fp8_quantize_swiglu": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp]),
+    "mg_fp8_quantize_weights": (_i32, [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "mg_moe_combine_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i64, _vp]),
+    "mg_moe_route": (_i32, [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                            _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "mg_moe_route_workspace": (_i64, [_i64, _i32]),
+    "mg_moe_route_bwd": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
+                                _i32, _vp]),
+    "mg_check_rows_host": (_i32, [_vp, _i64, _i64]),
     "mg_check_list_host": (_i32, [_vp, _i32]),
     "mg_status_str": (ctypes.c_char_p, [_i32]),
     "mg_abi_version": (_i32, []),

@@ -71,6 +71,22 @@ mg_status maybe_validate(const int32_t* offsets, int32_t E, int64_t M, hipStream
   return MG_OK;
 }
 
+// Under MGEMM_VALIDATE=1: every index in [0, M) of a token-to-row table at most
+// once (the combine's gradient writes each row from one place).
+mg_status maybe_validate_rows(const int32_t* token_rows, int64_t n, int64_t M, hipStream_t s) {
+  static const bool on = [] {
+    const char* v = std::getenv("MGEMM_VALIDATE");
+    return v != nullptr && v[0] == '1';
+  }();
+  if (!on) return MG_OK;
+  std::vector<int32_t> h(static_cast<size_t>(n));
+  if (hipMemcpyAsync(h.data(), token_rows, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, s) !=
+          hipSuccess ||
+      hipStreamSynchronize(s) != hipSuccess)
+    return MG_ERR_DEVICE;
+  return mg_check_rows_host(h.data(), n, M);
+}
+
 static_assert(sizeof(mg_gemm_desc) == sizeof(mg::ListDesc) &&
                   offsetof(mg_gemm_desc, m) == offsetof(mg::ListDesc, m) &&
                   offsetof(mg_gemm_desc, ldd) == offsetof(mg::ListDesc, ldd),
@@ -248,6 +264,53 @@ mg_status mgemm_fwd_mx(const void* x, const void* x_scale, const void* w, const 
   return launch(mg::kFwdMx, a, max_m_per_e, s);
 }
 
+namespace {
+
+// Shared body of the two block-scaled fp8 products.  `q8`, `qs`: x (forward)
+// or dy (input gradient) and its scales.
+mg_status fp8_product(bool dgrad, const void* q8, const float* qs, const void* w8, const float* ws,
+                      const int32_t* offsets, void* out, int64_t M, int64_t N, int64_t K, int32_t E,
+                      int64_t max_m_per_e, void* stream) {
+  mg_status st = check_sizes(M, N, K, E);
+  if (st != MG_OK) return st;
+  if (max_m_per_e < 0 || (N & 15) || (K & 15)) return MG_ERR_SHAPE;
+  const int64_t pdim = dgrad ? K : N, red = dgrad ? N : K;
+  // tile counts of the smallest tile (32 x 32) fit int32
+  if (((M + 31) / 32 + E) * ((pdim + 31) / 32) > kMaxRows) return MG_ERR_SHAPE;
+  if (M == 0 || pdim == 0) return MG_OK;
+  if (!offsets || !out || (red > 0 && (!q8 || !qs || !w8 || !ws))) return MG_ERR_NULL;
+  if ((red > 0 && (!aligned16(q8) || !aligned16(w8) || (reinterpret_cast<uintptr_t>(qs) & 3u) ||
+                   (reinterpret_cast<uintptr_t>(ws) & 3u))) ||
+      !aligned16(out) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+    return MG_ERR_ALIGN;
+  if ((st = check_device()) != MG_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = maybe_validate(offsets, E, M, s)) != MG_OK) return st;
+  mg::Fp8Args a{};
+  a.w8 = w8;
+  a.ws = ws;
+  a.q8 = q8;
+  a.qs = qs;
+  a.offsets = offsets;
+  a.out = out;
+  a.M = M; a.N = N; a.K = K; a.E = E;
+  return mg::launch_fp8(dgrad, a, max_m_per_e, s) == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
+}
+
+}  // namespace
+
+mg_status mgemm_fwd_fp8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
+                        const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int32_t E,
+                        int64_t max_m_per_e, void* stream) {
+  return fp8_product(false, x8, x_scale, w8, w_scale, offsets, y, M, N, K, E, max_m_per_e, stream);
+}
+
+mg_status mgemm_dgrad_fp8(const void* dy8, const float* dy_scale, const void* w8,
+                          const float* w_scale, const int32_t* offsets, void* dx, int64_t M,
+                          int64_t N, int64_t K, int32_t E, int64_t max_m_per_e, void* stream) {
+  return fp8_product(true, dy8, dy_scale, w8, w_scale, offsets, dx, M, N, K, E, max_m_per_e, stream);
+}
+
 mg_status kgemm_wgrad_mx_tm(const void* dy8, const void* dy_scale, const void* x8,
                             const void* x_scale, const int32_t* offsets, float* dw, int64_t M,
                             int64_t N, int64_t K, int32_t E, int32_t accumulate, void* stream) {
@@ -330,6 +393,167 @@ mg_status mg_moe_combine(const void* rows, const int32_t* token_rows, const floa
   const int err = mg::launch_moe_combine(static_cast<const uint16_t*>(rows), token_rows, weights,
                                          static_cast<uint16_t*>(out), M, T, k, D,
                                          static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
+}
+
+mg_status mg_moe_combine_bwd(const void* dout, const void* rows, const int32_t* token_rows,
+                             const float* weights, void* drows, float* dweights, int64_t M,
+                             int64_t T, int32_t k, int64_t D, void* stream) {
+  if (M < 0 || T < 0 || D < 0 || k < 1 || k > 64 || (D & 7) || M > kMaxRows || T > kMaxRows ||
+      D > kMaxDim)
+    return MG_ERR_SHAPE;
+  if (T == 0) return MG_OK;
+  if (!token_rows) return MG_ERR_NULL;
+  if (M > 0 && D > 0 && (!dout || !drows || (dweights != nullptr && !rows))) return MG_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) ||
+      (reinterpret_cast<uintptr_t>(token_rows) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dweights) & 3u))
+    return MG_ERR_ALIGN;
+  mg_status st;
+  if ((st = check_device()) != MG_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = maybe_validate_rows(token_rows, T * k, M, s)) != MG_OK) return st;
+  const int err = mg::launch_moe_combine_bwd(
+      static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(rows), token_rows, weights,
+      static_cast<uint16_t*>(drows), dweights, M, T, k, D, s);
+  return err == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
+}
+
+namespace {
+
+mg_status check_route(int64_t T, int32_t E, int32_t k) {
+  if (E < 1 || E > mg::kMaxExperts || k < 1 || k > 64 || k > E || T < 0 || T * k > kMaxRows)
+    return MG_ERR_SHAPE;
+  return MG_OK;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+int64_t mg_moe_route_workspace(int64_t T, int32_t E) {
+  return T < 0 || E < 1 || E > mg::kMaxExperts ? 0 : mg::route_workspace_bytes(T, E);
+}
+
+mg_status mg_moe_route(const void* logits, int32_t logits_bf16, const uint8_t* mask, int64_t T,
+                       int32_t E, int32_t k, int32_t normalize, int32_t first, int32_t local,
+                       float* weights, int32_t* experts, float* lse, int32_t* counts,
+                       float* prob_sum, int32_t* tokens, float* loss, int32_t* offsets,
+                       int32_t* gather, int32_t* token_rows, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  mg_status st = check_route(T, E, k);
+  if (st != MG_OK) return st;
+  if (first < 0 || local < 1 || first > E || local > E - first) return MG_ERR_SHAPE;
+  const int64_t need = mg::route_workspace_bytes(T, E);
+  if (need > 0 && workspace_bytes < need) return MG_ERR_SHAPE;
+  if (!counts || !prob_sum || !tokens || !loss || !offsets ||
+      (T > 0 && (!logits || !weights || !experts || !lse || !gather || !token_rows)) ||
+      (need > 0 && !workspace))
+    return MG_ERR_NULL;
+  if (misaligned4(counts) || misaligned4(prob_sum) || misaligned4(tokens) || misaligned4(loss) ||
+      misaligned4(offsets) || misaligned4(weights) || misaligned4(experts) || misaligned4(lse) ||
+      misaligned4(gather) || misaligned4(token_rows) || misaligned4(workspace) ||
+      (reinterpret_cast<uintptr_t>(logits) & (logits_bf16 ? 1u : 3u)))
+    return MG_ERR_ALIGN;
+  if ((st = check_device()) != MG_OK) return st;
+  mg::RouteArgs a{};
+  a.logits = logits;
+  a.mask = mask;
+  a.T = T;
+  a.E = E; a.k = k; a.normalize = normalize ? 1 : 0; a.first = first; a.local = local;
+  a.weights = weights; a.experts = experts; a.lse = lse;
+  a.counts = counts; a.prob_sum = prob_sum; a.tokens = tokens; a.loss = loss;
+  a.offsets = offsets; a.gather = gather; a.token_rows = token_rows;
+  a.workspace = workspace;
+  return mg::launch_route(a, logits_bf16 != 0, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? MG_OK
+             : MG_ERR_LAUNCH;
+}
+
+mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float* weights,
+                           const int32_t* experts, const float* lse, const int32_t* counts,
+                           const int32_t* tokens, const float* dweights, const float* dloss,
+                           void* dlogits, int64_t T, int32_t E, int32_t k, int32_t normalize,
+                           void* stream) {
+  mg_status st = check_route(T, E, k);
+  if (st != MG_OK) return st;
+  if (T == 0) return MG_OK;
+  if (!logits || !weights || !experts || !lse || !dlogits || (dloss && (!counts || !tokens)))
+    return MG_ERR_NULL;
+  const uintptr_t low = logits_bf16 ? 1u : 3u;
+  if ((reinterpret_cast<uintptr_t>(logits) & low) || (reinterpret_cast<uintptr_t>(dlogits) & low) ||
+      misaligned4(weights) || misaligned4(experts) || misaligned4(lse) || misaligned4(counts) ||
+      misaligned4(tokens) || misaligned4(dweights) || misaligned4(dloss))
+    return MG_ERR_ALIGN;
+  if ((st = check_device()) != MG_OK) return st;
+  mg::RouteBwdArgs a{};
+  a.logits = logits;
+  a.weights = weights; a.experts = experts; a.lse = lse;
+  a.counts = counts; a.tokens = tokens;
+  a.dweights = dweights; a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.T = T;
+  a.E = E; a.k = k; a.normalize = normalize ? 1 : 0;
+  return mg::launch_route_bwd(a, logits_bf16 != 0, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? MG_OK
+             : MG_ERR_LAUNCH;
+}
+
+namespace {
+
+// Shared body of the two row quantizers; `swiglu`: x holds g | u of 2 K columns.
+mg_status fp8_rows(bool swiglu, const void* x, int32_t x_fp32, const int32_t* gather,
+                   const int32_t* offsets, void* codes, float* scales, int64_t M, int64_t T,
+                   int64_t K, int32_t E, void* stream) {
+  if (M < 0 || T < 0 || K < 0 || M > kMaxRows || T > kMaxRows || K > kMaxDim || (K & 15) ||
+      (offsets != nullptr && (E < 1 || E > mg::kMaxExperts)))
+    return MG_ERR_SHAPE;
+  if (M == 0 || K == 0) return MG_OK;
+  if (!codes || !scales || (!x && (gather == nullptr || T > 0))) return MG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || misaligned4(scales) || misaligned4(gather) ||
+      misaligned4(offsets))
+    return MG_ERR_ALIGN;
+  mg_status st = check_device();
+  if (st != MG_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (offsets != nullptr && (st = maybe_validate(offsets, E, M, s)) != MG_OK) return st;
+  mg::Fp8RowsArgs a{};
+  a.x = x;
+  a.gather = gather;
+  a.offsets = offsets;
+  a.codes = codes;
+  a.scales = scales;
+  a.M = M; a.T = T; a.K = K; a.E = E;
+  return mg::launch_fp8_rows(a, x_fp32 != 0, swiglu, s) == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
+}
+
+}  // namespace
+
+mg_status mg_fp8_quantize(const void* x, int32_t x_fp32, const int32_t* gather,
+                          const int32_t* offsets, void* codes, float* scales, int64_t M, int64_t T,
+                          int64_t K, int32_t E, void* stream) {
+  return fp8_rows(false, x, x_fp32, gather, offsets, codes, scales, M, T, K, E, stream);
+}
+
+mg_status mg_fp8_quantize_swiglu(const void* gu, const int32_t* offsets, void* codes, float* scales,
+                                 int64_t M, int64_t I, int32_t E, void* stream) {
+  return fp8_rows(true, gu, 0, nullptr, offsets, codes, scales, M, M, I, E, stream);
+}
+
+mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, float* scales,
+                                  int64_t E, int64_t N, int64_t K, void* stream) {
+  if (E < 0 || N < 0 || K < 0 || E > kMaxRows || N > kMaxDim || K > kMaxDim || (K & 15))
+    return MG_ERR_SHAPE;
+  if (E * ((N + 127) / 128) > kMaxRows ||
+      E * ((N + 127) / 128) * ((K + 127) / 128) > kMaxRows)
+    return MG_ERR_SHAPE;
+  if (E == 0 || N == 0 || K == 0) return MG_OK;
+  if (!w || !codes || !scales) return MG_ERR_NULL;
+  if (!aligned16(w) || !aligned16(codes) || misaligned4(scales)) return MG_ERR_ALIGN;
+  mg_status st = check_device();
+  if (st != MG_OK) return st;
+  const int err = mg::launch_fp8_weights(w, w_fp32 != 0, static_cast<uint8_t*>(codes), scales, E, N,
+                                         K, static_cast<hipStream_t>(stream));
   return err == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
 }
 
@@ -425,6 +649,23 @@ mg_status mg_check_list_host(const mg_gemm_desc* desc_host, int32_t G) {
     if (d.m == 0 || d.n == 0) continue;
     if (!d.d || (d.k > 0 && (!d.a || !d.b))) return MG_ERR_NULL;
     if (!aligned16(d.d) || (d.k > 0 && (!aligned16(d.a) || !aligned16(d.b)))) return MG_ERR_ALIGN;
+  }
+  return MG_OK;
+}
+
+mg_status mg_check_rows_host(const int32_t* token_rows_host, int64_t n, int64_t M) {
+  if (!token_rows_host) return MG_ERR_NULL;
+  if (n < 0 || M < 0 || M > kMaxRows) return MG_ERR_SHAPE;
+  try {
+    std::vector<bool> seen(static_cast<size_t>(M), false);
+    for (int64_t i = 0; i < n; ++i) {
+      const int64_t r = token_rows_host[i];
+      if (r < 0 || r >= M) continue;
+      if (seen[static_cast<size_t>(r)]) return MG_ERR_OFFSETS;
+      seen[static_cast<size_t>(r)] = true;
+    }
+  } catch (...) {
+    return MG_ERR_DEVICE;                            // out of host memory
   }
   return MG_OK;
 }

@@ -78,4 +78,57 @@ int launch_moe_combine(const uint16_t* rows, const int32_t* token_rows, const fl
   return (int)hipGetLastError();
 }
 
+// Gradient of the combine.  One wave per (t, j): it reads dout[t] and
+// rows[r], r = token_rows[t, j], once, writes drows[r] = w dout[t] (one
+// rounding to bf16) and dweights[t, j] = <rows[r], dout[t]> (fp32, the lanes'
+// sums added in a fixed order).  HBM-bound; the k waves of a token sit in one
+// workgroup where k = 8, so dout[t] comes from HBM once.
+__global__ __launch_bounds__(512) void moe_combine_bwd_kernel(
+    const uint16_t* __restrict__ dout, const uint16_t* __restrict__ rows,
+    const int32_t* __restrict__ token_rows, const float* __restrict__ weights,
+    uint16_t* __restrict__ drows, float* __restrict__ dweights, int64_t M, int64_t total, int32_t k,
+    int64_t D) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t i = (int64_t)blockIdx.x * 8 + wave; i < total; i += (int64_t)gridDim.x * 8) {
+    const int64_t r = token_rows[i];
+    float dot = 0.0f;
+    if (r >= 0 && r < M) {
+      const float w = weights != nullptr ? weights[i] : 1.0f;
+      const uint16_t* dp = dout + (i / k) * D;
+      for (int64_t c = 8 * lane; c < D; c += 512) {
+        const u32x4_c d = *reinterpret_cast<const u32x4_c*>(dp + c);
+        u32x4_c v = {0u, 0u, 0u, 0u}, o;
+        if (dweights != nullptr) v = *reinterpret_cast<const u32x4_c*>(rows + r * D + c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float d0 = __builtin_bit_cast(float, d[q] << 16);
+          const float d1 = __builtin_bit_cast(float, d[q] & 0xFFFF0000u);
+          dot = __builtin_fmaf(d0, __builtin_bit_cast(float, v[q] << 16), dot);
+          dot = __builtin_fmaf(d1, __builtin_bit_cast(float, v[q] & 0xFFFF0000u), dot);
+          o[q] = __builtin_bit_cast(
+              uint32_t, __builtin_convertvector((f32x2_c){w * d0, w * d1}, bf16x2_c));
+        }
+        *reinterpret_cast<u32x4_c*>(drows + r * D + c) = o;
+      }
+    }
+    if (dweights != nullptr) {
+#pragma unroll
+      for (int s = 32; s >= 1; s >>= 1) dot += __shfl_xor(dot, s, 64);
+      if (lane == 0) dweights[i] = dot;
+    }
+  }
+}
+
+int launch_moe_combine_bwd(const uint16_t* dout, const uint16_t* rows, const int32_t* token_rows,
+                           const float* weights, uint16_t* drows, float* dweights, int64_t M,
+                           int64_t T, int32_t k, int64_t D, hipStream_t s) {
+  const int64_t total = T * k;
+  int64_t blocks = (total + 7) / 8;
+  if (blocks > 65536) blocks = 65536;                 // grid-stride beyond
+  hipLaunchKernelGGL(moe_combine_bwd_kernel, dim3((unsigned)blocks), dim3(512), 0, s, dout, rows,
+                     token_rows, weights, drows, dweights, M, total, k, D);
+  return (int)hipGetLastError();
+}
+
 }  // namespace mg

@@ -61,6 +61,81 @@ int launch_moe_combine(const uint16_t* rows, const int32_t* token_rows, const fl
 int launch_mx_scales_blocked(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t K,
                              int64_t batch, hipStream_t s);
 
+// Block-scaled fp8 products: E4M3 codes, one fp32 scale per row and 128
+// reduction steps of q8, one per 128 x 128 block of w8.
+struct Fp8Args {
+  const void* w8;           // [E, N, K]
+  const float* ws;          // [E, ceil(N/128), ceil(K/128)]
+  const void* q8;           // forward: x8 [M, K]; input gradient: dy8 [M, N]
+  const float* qs;          // forward: [ceil(K/128), M]; input gradient: [ceil(N/128), M]
+  const int32_t* offsets;   // [E+1], device
+  void* out;                // bf16: y [M, N] or dx [M, K]
+  int64_t M, N, K;
+  int32_t E;
+};
+int launch_fp8(bool dgrad, const Fp8Args& a, int64_t max_m_per_e, hipStream_t s);
+
+// Rows to block-scaled fp8: codes [M, K], scales [ceil(K/128), M]; with
+// `gather`, row i is row gather[i] of x [T, K]; with `offsets` (E entries + 1,
+// device) only rows below offsets[E] are written.  With swiglu x is g | u
+// [M, 2 K] (bf16) and the values silu(g) u.
+struct Fp8RowsArgs {
+  const void* x;
+  const int32_t* gather;
+  const int32_t* offsets;
+  void* codes;
+  float* scales;
+  int64_t M, T, K;
+  int32_t E;
+};
+int launch_fp8_rows(const Fp8RowsArgs& a, bool fp32, bool swiglu, hipStream_t s);
+// Weights [E, N, K] to codes [E, N, K] and scales [E, ceil(N/128), ceil(K/128)].
+int launch_fp8_weights(const void* w, bool fp32, uint8_t* codes, float* scales, int64_t E, int64_t N,
+                       int64_t K, hipStream_t s);
+
+// Router forward (see mg_moe_route); per_group is set by the launch.
+struct RouteArgs {
+  const void* logits;       // [T, E] fp32 or bf16
+  const uint8_t* mask;      // [T] or NULL
+  int64_t T;
+  int32_t E, k, normalize, first, local;
+  float* weights;           // [T, k]
+  int32_t* experts;         // [T, k]
+  float* lse;               // [T]
+  int32_t* counts;          // [E]
+  float* prob_sum;          // [E]
+  int32_t* tokens;          // [1]
+  float* loss;              // [2]
+  int32_t* offsets;         // [local + 1]
+  int32_t* gather;          // [T k]
+  int32_t* token_rows;      // [T, k]
+  void* workspace;
+  int64_t per_group;        // tokens per workgroup of the token pass
+};
+int64_t route_workspace_bytes(int64_t T, int32_t E);
+int launch_route(const RouteArgs& a, bool bf16, hipStream_t s);
+
+struct RouteBwdArgs {
+  const void* logits;       // [T, E] fp32 or bf16
+  const float* weights;     // [T, k]
+  const int32_t* experts;   // [T, k]
+  const float* lse;         // [T]
+  const int32_t* counts;    // [E]
+  const int32_t* tokens;    // [1]
+  const float* dweights;    // [T, k] or NULL
+  const float* dloss;       // [2] or NULL
+  void* dlogits;            // [T, E] as the logits
+  int64_t T;
+  int32_t E, k, normalize;
+};
+int launch_route_bwd(const RouteBwdArgs& a, bool bf16, hipStream_t s);
+
+// Gradient of the token-order combine: drows[token_rows[t, j]] = w[t, j] dout[t]
+// and, with weights, dweights[t, j] = <rows[token_rows[t, j]], dout[t]>.
+int launch_moe_combine_bwd(const uint16_t* dout, const uint16_t* rows, const int32_t* token_rows,
+                           const float* weights, uint16_t* drows, float* dweights, int64_t M,
+                           int64_t T, int32_t k, int64_t D, hipStream_t s);
+
 // Where the weight gradient's token split takes its workspace from.
 enum WsKind {
   kWsStream = 0,   // a device allocation per (device, stream), made on first use

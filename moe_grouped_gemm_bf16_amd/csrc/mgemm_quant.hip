@@ -1,0 +1,232 @@
+// Block-scaled fp8 quantizers: values to E4M3 codes with one fp32 scale per
+// row and 128 columns (activations) or per 128 x 128 block (weights):
+//   a = max(max |x| over the block, 2^-100),  scale = a / 448,
+//   code = e4m3(x (448 / a))            (448: the largest E4M3 value)
+// with both quotients correctly rounded fp32 divisions and the product rounded
+// once to fp32 and once, to nearest even, to E4M3.  The floor 2^-100 keeps
+// 448 / a finite; a block of zeros gets it and zero codes.  A NaN, or an
+// infinity (whose scale is infinite), gives NaN codes, so the outputs of that
+// row's products are NaN and no other row's.
+//
+// HBM-bound (2 bytes in, 1 byte out per bf16 value): 16 lanes hold one block's
+// 128 columns, 8 each, so its maximum is four lane-row rotations away, and a
+// workgroup's eight blocks per lane group are loaded before the first is used.
+// The scales, whose rows run along M, leave through LDS as 128-byte runs.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mgemm_launch.h"
+
+namespace mg {
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kTop = 448.0f;
+constexpr float kFloor = 0x1p-100f;
+
+template <int CTRL>
+__device__ __forceinline__ float rotate_max(float x) {
+  const int y = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false);
+  return fmaxf(x, __builtin_bit_cast(float, y));
+}
+// Maximum over the 16 lanes of a lane row.
+__device__ __forceinline__ float row_max(float x) {
+  x = rotate_max<0x128>(x);
+  x = rotate_max<0x124>(x);
+  x = rotate_max<0x122>(x);
+  return rotate_max<0x121>(x);
+}
+
+// Eight values as loaded: bf16 (one 16-byte piece) or fp32 (two).
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void to(float (&f)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = __builtin_bit_cast(float, v[q] << 16);
+      f[2 * q + 1] = __builtin_bit_cast(float, v[q] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  f32x4 lo, hi;
+  __device__ __forceinline__ void zero() { lo = hi = f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void load(const float* p) {
+    lo = *reinterpret_cast<const f32x4*>(p);
+    hi = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  __device__ __forceinline__ void to(float (&f)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[q] = lo[q];
+      f[4 + q] = hi[q];
+    }
+  }
+};
+
+__device__ __forceinline__ float abs_max8(const float (&f)[8]) {
+  float a = fabsf(f[0]);
+#pragma unroll
+  for (int q = 1; q < 8; ++q) a = fmaxf(a, fabsf(f[q]));
+  return a;
+}
+
+__device__ __forceinline__ u32x2 encode8(const float (&f)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
+    w[h] = (uint32_t)v;
+  }
+  return u32x2{w[0], w[1]};
+}
+
+// Rows: a workgroup takes 32 rows x 4 blocks; wave w rows 8 w .. + 7, its four
+// lane rows the four blocks.  SWI: x holds g | u of 2 K columns and the value
+// is silu(g) u.
+constexpr int kRows = 32, kBlocks = 4;
+
+template <typename T, bool SWI>
+__global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8RowsArgs a) {
+  __shared__ float scales[kBlocks][kRows];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int blk = lane >> 4;
+  const int64_t nb = (a.K + 127) / 128;
+  const int64_t b0 = (int64_t)blockIdx.y * kBlocks;
+  const int64_t col = (b0 + blk) * 128 + 8 * (lane & 15);
+  int64_t end = a.M;
+  if (a.offsets != nullptr) {
+    const int64_t o = a.offsets[a.E];
+    end = o < 0 ? 0 : (o < end ? o : end);
+  }
+  const T* x = static_cast<const T*>(a.x);
+  const int64_t ld = SWI ? 2 * a.K : a.K;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < end; r0 += (int64_t)gridDim.x * kRows) {
+    Eight<T> v[8], u[SWI ? 8 : 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + 8 * wave + i;
+      v[i].zero();
+      if (SWI) u[SWI ? i : 0].zero();
+      if (r < end && col < a.K) {
+        int64_t src = r;
+        if (!SWI && a.gather != nullptr) {
+          src = a.gather[r];
+          if (src >= a.T) src = -1;                    // an index out of range: a row of zeros
+        }
+        if (src >= 0) {
+          v[i].load(x + src * ld + col);
+          if (SWI) u[SWI ? i : 0].load(x + src * ld + a.K + col);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      v[i].to(f);
+      if (SWI) {
+        float w[8];
+        u[SWI ? i : 0].to(w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float ex = __builtin_amdgcn_exp2f(-f[q] * 1.4426950408889634f);
+          f[q] = f[q] * __builtin_amdgcn_rcpf(1.0f + ex) * w[q];
+        }
+      }
+      const float am = fmaxf(row_max(abs_max8(f)), kFloor);
+      const int64_t r = r0 + 8 * wave + i;
+      const u32x2 c = encode8(f, kTop / am);
+      if (r < end && col < a.K)
+        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.codes) + r * a.K + col) = c;
+      if ((lane & 15) == 0) scales[blk][8 * wave + i] = am / kTop;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBlocks * kRows) {
+      const int b = threadIdx.x / kRows, r = threadIdx.x % kRows;
+      if (b0 + b < nb && r0 + r < end) a.scales[(b0 + b) * a.M + r0 + r] = scales[b][r];
+    }
+    __syncthreads();
+  }
+}
+
+// Weights: a workgroup takes one 128 x 128 block, 16 lanes per row, eight rows
+// per lane, and finds the block's maximum through LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void fp8_weights_kernel(const T* __restrict__ w,
+                                                          uint8_t* __restrict__ codes,
+                                                          float* __restrict__ scales, int64_t N,
+                                                          int64_t K) {
+  __shared__ float part[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t nk = (K + 127) / 128, nn = (N + 127) / 128;
+  const int64_t kb = blockIdx.x % nk, en = blockIdx.x / nk;
+  const int64_t e = en / nn, n0 = (en - e * nn) * 128;
+  const int64_t col = kb * 128 + 8 * (lane & 15);
+  Eight<T> v[8];
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = n0 + 16 * i + 4 * wave + (lane >> 4);
+    v[i].zero();
+    if (n < N && col < K) v[i].load(w + (e * N + n) * K + col);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    v[i].to(f);
+    am = fmaxf(am, abs_max8(f));
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) am = fmaxf(am, __shfl_xor(am, d, 64));
+  if (lane == 0) part[wave] = am;
+  __syncthreads();
+  am = fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])), kFloor);
+  const float inv = kTop / am;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = n0 + 16 * i + 4 * wave + (lane >> 4);
+    float f[8];
+    v[i].to(f);
+    if (n < N && col < K) *reinterpret_cast<u32x2*>(codes + (e * N + n) * K + col) = encode8(f, inv);
+  }
+  if (threadIdx.x == 0) scales[en * nk + kb] = am / kTop;
+}
+
+}  // namespace
+
+int launch_fp8_rows(const Fp8RowsArgs& a, bool fp32, bool swiglu, hipStream_t s) {
+  const int64_t nb = (a.K + 127) / 128;
+  int64_t gx = (a.M + kRows - 1) / kRows;
+  const int64_t gy = (nb + kBlocks - 1) / kBlocks;
+  if (gx > 65536) gx = 65536;                           // grid-stride beyond
+  const dim3 g((unsigned)gx, (unsigned)gy), b(256);
+  if (swiglu) hipLaunchKernelGGL((fp8_rows_kernel<uint16_t, true>), g, b, 0, s, a);
+  else if (fp32) hipLaunchKernelGGL((fp8_rows_kernel<float, false>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((fp8_rows_kernel<uint16_t, false>), g, b, 0, s, a);
+  return (int)hipGetLastError();
+}
+
+int launch_fp8_weights(const void* w, bool fp32, uint8_t* codes, float* scales, int64_t E, int64_t N,
+                       int64_t K, hipStream_t s) {
+  const int64_t blocks = E * ((N + 127) / 128) * ((K + 127) / 128);
+  const dim3 g((unsigned)blocks), b(256);
+  if (fp32)
+    hipLaunchKernelGGL((fp8_weights_kernel<float>), g, b, 0, s, static_cast<const float*>(w), codes,
+                       scales, N, K);
+  else
+    hipLaunchKernelGGL((fp8_weights_kernel<uint16_t>), g, b, 0, s, static_cast<const uint16_t*>(w),
+                       codes, scales, N, K);
+  return (int)hipGetLastError();
+}
+
+}  // namespace mg
