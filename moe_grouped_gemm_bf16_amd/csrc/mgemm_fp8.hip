@@ -50,19 +50,38 @@ __device__ __forceinline__ i32x4 rsrc_of(const void* base, uint32_t bytes) {
   return r;
 }
 
-// Direct-to-LDS loads: lane l's 16 (4) bytes land at lds_addr + 16 l (4 l).
-// Awaited with vmcnt(0) before the barrier that publishes the stage.
-__device__ __forceinline__ void to_lds16(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
+// Direct-to-LDS loads of one stage: four 1-KiB pieces of P, four of Q (lane
+// l's 16 bytes of piece j land at lds + 1024 j + 16 l) and one dword per lane
+// of the scales.  One block, so that m0, which holds the LDS address, is saved
+// and restored once (the scalar unit is a third of the loop's issue slots when
+// every load does it); a wait state separates each m0 write from its load.
+// Awaited with vmcnt before the barrier that publishes the stage.
+__device__ __forceinline__ void load_stage(const i32x4& rp, const i32x4& rq, const i32x4& rs,
+                                           uint32_t lp, uint32_t lq, uint32_t ls,
+                                           const uint32_t (&vp)[4], const uint32_t (&vq)[4],
+                                           uint32_t vs) {
   uint32_t save;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
-               "s_mov_b32 m0, %0"
-               : "=&s"(save) : "s"(lds_addr), "v"(voff), "s"(rsrc) : "memory");
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %13, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %13, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %13, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %13, 0 offen lds\n\t"
+      "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %8, %14, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %9, %14, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %10, %14, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %11, %14, 0 offen lds\n\t"
+      "s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %12, %15, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(save)
+      : "s"(lp), "s"(lq), "s"(ls), "v"(vp[0]), "v"(vp[1]), "v"(vp[2]), "v"(vp[3]), "v"(vq[0]),
+        "v"(vq[1]), "v"(vq[2]), "v"(vq[3]), "v"(vs), "s"(rp), "s"(rq), "s"(rs)
+      : "memory", "scc");
 }
-__device__ __forceinline__ void to_lds4(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
-  uint32_t save;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, 0 offen lds\n\t"
-               "s_mov_b32 m0, %0"
-               : "=&s"(save) : "s"(lds_addr), "v"(voff), "s"(rsrc) : "memory");
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_addr_of(const void* p) {
@@ -136,46 +155,96 @@ struct Tile {
 
 // Tile id L -> tile: expert by expert, inside an expert in groups of gm
 // M-tiles (M-tile fastest, then P-tile), so that the tiles that run at the
-// same time on one XCD share weight and activation panels in its L2.
+// same time on one XCD share weight and activation panels in its L2.  Ids are
+// asked for in ascending order: the expert search goes on from the last one.
 template <int BP, int BQ>
-__device__ __forceinline__ Tile tile_of(int L, const Experts& X, int tilesP, int gm) {
-  int lo = 0, hi = X.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (X.pref[mid] * tilesP <= L) lo = mid; else hi = mid - 1;
+struct Decode {
+  int first = 0, after = 0;                 // the current expert's tile ids,
+  int e = 0, lo = 0, hi = 0;                // index and rows
+  uint32_t group, rcp;                      // tiles of a full group, 2^32 / group
+  __device__ __forceinline__ void init(int tilesP, int gm) {
+    group = (uint32_t)gm * (uint32_t)tilesP;
+    rcp = __builtin_amdgcn_readfirstlane(0xFFFFFFFFu / group);
   }
-  const int e = __builtin_amdgcn_readfirstlane(lo);
-  const int local = L - X.pref[e] * tilesP;
-  const int mt = X.pref[e + 1] - X.pref[e];
-  const int g = local / (gm * tilesP);
-  const int rem = local - g * gm * tilesP;
-  const int gh = min(gm, mt - g * gm);
-  const int tp = rem / gh;
-  Tile t;
-  t.e = e;
-  t.q0 = __builtin_amdgcn_readfirstlane(X.offs[e] + (g * gm + rem - tp * gh) * BQ);
-  t.q_end = __builtin_amdgcn_readfirstlane(X.offs[e + 1]);
-  t.p0 = __builtin_amdgcn_readfirstlane(tp * BP);
-  return t;
-}
+  __device__ __forceinline__ Tile at(int L, const Experts& X, int tilesP, int gm) {
+    if (L >= after) {
+      int a = e, b = X.E - 1;
+      while (a < b) {
+        const int mid = (a + b + 1) >> 1;
+        if (X.pref[mid] * tilesP <= L) a = mid; else b = mid - 1;
+      }
+      e = __builtin_amdgcn_readfirstlane(a);
+      first = __builtin_amdgcn_readfirstlane(X.pref[e]) * tilesP;
+      after = __builtin_amdgcn_readfirstlane(X.pref[e + 1]) * tilesP;
+      lo = __builtin_amdgcn_readfirstlane(X.offs[e]);
+      hi = __builtin_amdgcn_readfirstlane(X.offs[e + 1]);
+    }
+    const uint32_t local = (uint32_t)(L - first);
+    // local / group: the estimate from the reciprocal is at most two low
+    uint32_t g = __umulhi(local, rcp), rem = local - g * group;
+    if (rem >= group) { ++g; rem -= group; }
+    if (rem >= group) { ++g; rem -= group; }
+    const int mt = (hi - lo + BQ - 1) / BQ;
+    const uint32_t gh = (uint32_t)min(gm, mt - (int)g * gm);
+    const uint32_t tp = rem / gh;
+    Tile t;
+    t.e = e;
+    t.q0 = lo + ((int)g * gm + (int)(rem - tp * gh)) * BQ;
+    t.q_end = hi;
+    t.p0 = (int)tp * BP;
+    return t;
+  }
+};
 
-// Workgroup b runs on XCD b % 8; every XCD takes a contiguous range of tile
-// ids, its workgroups every nx-th of them.
-struct Walk {
-  int at, end, step;
-  __device__ __forceinline__ void init(int total) {
-    const int x = blockIdx.x & 7, c = blockIdx.x >> 3;
+// The tiles of this workgroup.  Workgroup b runs on XCD b % 8; every XCD takes
+// a contiguous range of tile ids, its nx workgroups every nx-th of them.  Where
+// the last round has at most nx / 2 tiles, HALVES gives each to two workgroups
+// of half the rows (a tile's time follows its rows, see the row skip of the
+// tiled kernel), so a round that is a quarter full costs half a round.
+template <int BP, int BQ, bool HALVES>
+struct Items {
+  Decode<BP, BQ> dec;
+  int i, items, lo, full, step;
+  bool halves;
+  __device__ __forceinline__ void init(int total, int tilesP, int gm) {
+    dec.init(tilesP, gm);
+    const int x = blockIdx.x & 7;
     const int q8 = total >> 3, r8 = total & 7;
-    const int lo = x * q8 + min(x, r8);
-    end = lo + q8 + (x < r8 ? 1 : 0);
-    at = lo + c;
+    const int count = q8 + (x < r8 ? 1 : 0);
+    lo = x * q8 + min(x, r8);
     step = gridDim.x >> 3;
+    full = HALVES ? count / step * step : count;
+    const int rest = count - full;
+    halves = HALVES && 2 * rest <= step;
+    items = full + (halves ? 2 * rest : rest);
+    i = blockIdx.x >> 3;
+  }
+  // The next tile, or false behind the last; halves without rows are passed over.
+  __device__ __forceinline__ bool next(const Experts& X, int tilesP, int gm, Tile& t) {
+    bool found = false;
+    while (!found && i < items) {
+      const int u = i - full;
+      const bool half = halves && u >= 0;
+      t = dec.at(lo + (half ? full + (u >> 1) : i), X, tilesP, gm);
+      i += step;
+      if (half) {
+        t.q0 += (u & 1) * (BQ / 2);
+        t.q_end = min(t.q_end, t.q0 + BQ / 2);
+      }
+      found = __builtin_amdgcn_readfirstlane(t.q0 < t.q_end);
+    }
+    t.q0 = __builtin_amdgcn_readfirstlane(t.q0);
+    t.q_end = __builtin_amdgcn_readfirstlane(t.q_end);
+    t.p0 = __builtin_amdgcn_readfirstlane(t.p0);
+    i = __builtin_amdgcn_readfirstlane(i);
+    return found;
   }
 };
 
 // ------------------------------------------------------------- tiled kernel --
 
-// BP x BQ output tile, WP x WQ waves; kStages LDS stages of 128 steps.
+// BP x BQ output tile, WP x WQ waves; ST LDS stages of 128 steps.  Every wave
+// loads four 1-KiB pieces of the P tile and four of the Q tile of a stage.
 template <int BP_, int BQ_, int WP_, int WQ_, int ST_>
 struct Fp8Cfg {
   static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, ST = ST_;
@@ -183,15 +252,17 @@ struct Fp8Cfg {
   static constexpr int WTP = BP / WP, WTQ = BQ / WQ, MP = WTP / 16, MQ = WTQ / 16;
   static constexpr int P_BYTES = BP * kBlk, DATA = (BP + BQ) * kBlk;
   static constexpr int SCALES = NW * 256, STAGE = DATA + SCALES;
-  static constexpr int SPW = DATA / 1024 / NW;           // 1 KiB loads per wave and stage
-  static constexpr int SEGS_P = P_BYTES / 1024;
-  static_assert(DATA / 1024 % NW == 0 && SEGS_P % SPW == 0 && SPW % 4 == 0, "loads per wave");
-  static_assert(MP % 4 == 0 && WTP <= 128 && 128 % WTP == 0, "one weight scale per wave");
+  static constexpr int LOADS = 9;                        // per wave and stage (load_stage)
+  static constexpr int AHEAD = MP == 8 ? 1 : 2;          // P fragments read ahead
+  static constexpr int RING = AHEAD == 1 ? 2 : 4;        // and their registers
+  static_assert(BP == 32 * NW && BQ == 32 * NW, "load_stage: four segments of each operand");
+  static_assert(MP % 4 == 0 && MQ % 2 == 0 && WTP <= 128 && 128 % WTP == 0, "wave tile");
   static_assert(BQ / 64 + 1 <= NW && BQ % 64 == 0, "scale loads");
+  static_assert((MP - 1) % RING != 0, "the next stage's first fragment has a free slot");
 };
 
 template <bool DG, class C>
-__global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
+__global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
   __shared__ __attribute__((aligned(16))) char lds[C::ST * C::STAGE];
   __shared__ int sched[2 * (kMaxExperts + 1)];
   // reduction length, output width, leading dimensions of the code arrays
@@ -210,111 +281,140 @@ __global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  // (waves w and w + 4 share a SIMD: this order spreads the first half of the
+  // rows over all four)
+  const int wp = wave % C::WP, wq = wave / C::WP;
   const int l16 = lane & 15, g4 = lane >> 4;
 
-  // ---- producer: stage loads of this wave, 1 KiB segments seg0 .. + SPW of
-  // its operand's tile.  Steps-contiguous tiles are [rows][128] bytes in
-  // 16-byte chunks, chunk c of row r at c ^ (r % 8) ^ (r / 8 % 4): 16 rows
-  // read at one chunk hit 16 distinct 16-byte banks.  DGRAD's weights are
-  // staged as they lie, [128 n][BP k], chunk c of row r at
-  // c ^ (2 (r % 8)) ^ (r / 32 % 2) (BP = 256) or
-  // c ^ (2 (r / 2 % 4)) ^ (r / 32 % 2) (BP = 128): the transpose reads of 8
-  // rows by two lane groups, 32 rows apart, then hit 16 distinct banks.
-  const bool isP = wave * C::SPW < C::SEGS_P;
-  const int seg0 = isP ? wave * C::SPW : wave * C::SPW - C::SEGS_P;
+  // ---- producer.  Steps-contiguous tiles are [rows][128] bytes in 16-byte
+  // chunks, chunk c of row r at c ^ (r % 8) ^ (r / 8 % 4): 16 rows read at one
+  // chunk hit 16 distinct 16-byte banks.  DGRAD's weights are staged as they
+  // lie, [128 n][BP k], chunk c of row r at c ^ (2 (r % 8)) ^ (r / 32 % 2)
+  // (BP = 256) or c ^ (2 (r / 2 % 4)) ^ (r / 32 % 2) (BP = 128): the transpose
+  // reads of 8 rows by two lane groups, 32 rows apart, then hit 16 distinct
+  // banks.  The lane's offsets are the same for every tile and stage; the
+  // descriptors move.
   const uint32_t lds0 = lds_addr_of(lds);
-  const uint32_t data0 = lds0 + (isP ? 0u : (uint32_t)C::P_BYTES) + (uint32_t)seg0 * 1024u;
-  const uint32_t scale0 = lds0 + (uint32_t)C::DATA + (uint32_t)wave * 256u;
-  const int ld = isP ? ldP : ldQ;
-  const bool strided = DG && isP;
-  constexpr int RPS = 1024 / (DG ? C::BP : kBlk);          // strided: rows per segment
-  const int c0 = (lane & 7) ^ (lane >> 3);
-  const uint32_t row0 = strided ? (uint32_t)(seg0 * RPS + lane / (C::BP / 16)) * (uint32_t)ld
-                                : (uint32_t)(seg0 * 8 + (lane >> 3)) * (uint32_t)ld;
+  // Piece j of the wave's four of an operand lies 8 rows (DGRAD's weights:
+  // 1024 / BP) below piece j - 1, and its chunk differs from piece 0's by an
+  // exclusive or, so the eight offsets take few operations and no register
+  // between stages (a wave's 128 accumulators leave room for none).
+  constexpr int CPR = DG ? C::BP / 16 : 8;                 // chunks per row of P
+  // (BP = 256: rows 4 apart; 128: rows 8 apart, the same chunk; else r / 8 % 4)
+  auto pxor = [](int j) { return !DG ? 16 * j : C::BP == 256 ? 128 * (j & 1) : 0; };
 
-  Walk pw;
-  pw.init(total);
+  Items<C::BP, C::BQ, true> items;
+  items.init(total, tilesP, gm);
+  // tiles that the producer has begun and the consumer not yet: with a
+  // reduction of one stage the producer is ST tiles ahead
+  Tile ahead[C::ST + 1];
+  int nahead = 0;
   bool live = false;
-  const uint8_t* psrc = nullptr;     // the operand's tile at reduction step 0
-  const float* pscale = nullptr;     // the wave's scales at block 0
-  int64_t pscale_step = 0;
-  uint32_t psc_off = kOOB;           // this lane's scale, bytes from pscale
-  uint32_t psc_range = 0;
-  int pouter = 0, pkt = 0, produced = 0;
+  // the next stage's descriptors, advanced by a stage's bytes each time
+  i32x4 rp = {0, 0, 0, 0x00020000}, rq = rp, rs = rp;
+  const int64_t stepP = DG ? (int64_t)kBlk * ldP : kBlk;
+  int64_t stepS = 0;                 // bytes between the wave's scales of two blocks
+  uint32_t vs = kOOB;                // this lane's scale
+  int outP = 0, pleft = 0, produced = 0;
+  uint32_t pbuf = 0;
+  auto advance = [](i32x4& r, int64_t bytes) {
+    const uint64_t b = (((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x) + (uint64_t)bytes;
+    r.x = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    r.y = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  };
   auto next_tile = [&]() {
-    live = pw.at < pw.end && nk > 0;
+    Tile t = {0, 0, 0, 0};
+    live = items.next(X, tilesP, gm, t);
     if (!live) return;
-    const Tile t = tile_of<C::BP, C::BQ>(pw.at, X, tilesP, gm);
-    pw.at += pw.step;
-    pkt = 0;
+#pragma unroll
+    for (int u = 0; u <= C::ST; ++u)
+      if (u == nahead) ahead[u] = t;
+    ++nahead;
+    pleft = red;
     const uint8_t* w = static_cast<const uint8_t*>(a.w8) + (int64_t)t.e * a.N * a.K;
-    if (isP) {
-      psrc = DG ? w + t.p0 : w + (int64_t)t.p0 * a.K;
-      pouter = min(Pdim - t.p0, C::BP);
-    } else {
-      psrc = static_cast<const uint8_t*>(a.q8) + (int64_t)t.q0 * ldQ;
-      pouter = min(t.q_end - t.q0, C::BQ);
-    }
+    outP = __builtin_amdgcn_readfirstlane(min(Pdim - t.p0, C::BP));
+    const int outQ = min(t.q_end - t.q0, C::BQ);
+    // Ranges end a stage's columns after the last valid row's start, so rows
+    // past it are out of range (a row is at least that long) while the base
+    // moves; columns past the reduction's (or DGRAD's output's) end are put
+    // out of range by their lanes' offsets (see produce).
+    const uint32_t cols = (uint32_t)min(red, kBlk);
+    rp = rsrc_of(DG ? w + t.p0 : w + (int64_t)t.p0 * a.K,
+                 DG ? (uint32_t)(kBlk - 1) * (uint32_t)ldP + (uint32_t)outP
+                    : (uint32_t)(outP - 1) * (uint32_t)ldP + cols);
+    rq = rsrc_of(static_cast<const uint8_t*>(a.q8) + (int64_t)t.q0 * ldQ,
+                 (uint32_t)(outQ - 1) * (uint32_t)ldQ + cols);
     // scales: waves 0 .. BQ/64 - 1 load 64 rows' each, the next wave the
-    // weights' (one per 128 P indices); the other waves load nothing
-    psc_off = kOOB;
-    psc_range = 0;
+    // weights' (one per 128 P indices); the other waves' load reads nothing
+    const float* s = a.qs;
+    uint32_t range = 0;
+    vs = kOOB;
+    stepS = 0;
     if (wave < C::BQ / 64) {
-      pscale = a.qs + t.q0;
-      pscale_step = a.M;
-      const int rows = min((int)a.M - t.q0, C::BQ);
-      psc_range = (uint32_t)rows * 4u;
-      psc_off = (uint32_t)(wave * 64 + lane) * 4u;
+      s = a.qs + t.q0;
+      stepS = 4 * a.M;
+      range = (uint32_t)min((int)a.M - t.q0, C::BQ) * 4u;
+      vs = (uint32_t)(wave * 64 + lane) * 4u;
     } else if (wave == C::BQ / 64) {
       const int pb = t.p0 / kBlk;
-      const float* s = a.ws + (int64_t)t.e * nn * nkb;
       const int blocks = min((C::BP + kBlk - 1) / kBlk, (DG ? nkb : nn) - pb);
-      pscale = DG ? s + pb : s + (int64_t)pb * nkb;
-      pscale_step = DG ? nkb : 1;
       const uint32_t step = DG ? 4u : (uint32_t)nkb * 4u;
-      psc_range = (uint32_t)(blocks - 1) * step + 4u;
-      if (lane < blocks) psc_off = (uint32_t)lane * step;
-    } else {
-      pscale = a.qs;
-      pscale_step = 0;
+      s = a.ws + (int64_t)t.e * nn * nkb + (DG ? (int64_t)pb : (int64_t)pb * nkb);
+      stepS = DG ? 4 * (int64_t)nkb : 4;
+      range = (uint32_t)(blocks - 1) * step + 4u;
+      if (lane < blocks) vs = (uint32_t)lane * step;
     }
+    rs = rsrc_of(s, range);
   };
-  // Issue the producer's next stage into LDS stage buffer produced % ST.
+  // Issue the producer's next stage into the LDS buffer that is free.
   auto produce = [&]() {
-    if (!live) return;
-    const int r0 = pkt * kBlk;
-    const uint32_t buf = (uint32_t)(produced % C::ST) * (uint32_t)C::STAGE;
-    i32x4 rs;
-    if (strided) {
-      const int rr = min(red - r0, kBlk);
-      rs = rsrc_of(psrc + (int64_t)r0 * ld, (uint32_t)(rr - 1) * (uint32_t)ld + (uint32_t)pouter);
-    } else {
-      rs = rsrc_of(psrc + r0, (uint32_t)(pouter - 1) * (uint32_t)ld + (uint32_t)min(red - r0, kBlk));
-    }
-    const i32x4 ss = rsrc_of(pscale + pkt * pscale_step, psc_range);
-    // (an opaque copy: the loads' offsets are not kept in registers between stages)
-    uint32_t ro = row0;
-    asm volatile("" : "+v"(ro));
+    if (!live || nk == 0) return;
+    const uint32_t buf = lds0 + pbuf;
+    const uint32_t lp = buf + (uint32_t)(wave * 4) * 1024u;
+    const uint32_t lq = buf + (uint32_t)C::P_BYTES + (uint32_t)(wave * 4) * 1024u;
+    const uint32_t ls = buf + (uint32_t)C::DATA + (uint32_t)wave * 256u;
+    const bool tail = pleft < kBlk;
+    uint32_t vp[4], vq[4];
+    uint32_t ln = (uint32_t)lane;
+    asm volatile("" : "+v"(ln));                 // (what follows is not kept between stages)
+    const int prow = wave * (4 * 64 / CPR) + (int)(ln / CPR);
+    const int psw = !DG ? (prow & 7) ^ ((prow >> 3) & 3)
+                        : C::BP == 256 ? (2 * (prow & 7)) ^ ((prow >> 5) & 1)
+                                       : (2 * ((prow >> 1) & 3)) ^ ((prow >> 5) & 1);
+    const int qrow = wave * 32 + (int)(ln >> 3);
+    const int pc0 = 16 * ((int)(ln % CPR) ^ psw);
+    const int qc0 = 16 * ((int)(ln & 7) ^ (qrow & 7) ^ ((qrow >> 3) & 3));
+    const uint32_t pb = (uint32_t)prow * (uint32_t)ldP;
 #pragma unroll
-    for (int j = 0; j < C::SPW; ++j) {
-      uint32_t off;
-      if (strided) {
-        const int seg = seg0 + j, row = seg * RPS + lane / (C::BP / 16);
-        const int sw = C::BP == 256 ? (2 * (row & 7)) ^ ((row >> 5) & 1)
-                                    : (2 * ((row >> 1) & 3)) ^ ((row >> 5) & 1);
-        const int col = 16 * ((lane % (C::BP / 16)) ^ sw);
-        off = (ro + (uint32_t)(j * RPS) * (uint32_t)ld + (uint32_t)col) | (col < pouter ? 0u : kOOB);
-      } else {
-        const int col = 16 * (c0 ^ (j & 3));
-        off = (ro + (uint32_t)(j * 8) * (uint32_t)ld + (uint32_t)col) |
-              (r0 + col < red ? 0u : kOOB);
-      }
-      to_lds16(rs, data0 + buf + (uint32_t)j * 1024u, off);
+    for (int j = 0; j < 4; ++j) {
+      vp[j] = pb + (uint32_t)(j * (64 / CPR)) * (uint32_t)ldP + (uint32_t)(pc0 ^ pxor(j));
+      // FWD: both operands are rows of K steps, and the offsets are the same
+      vq[j] = !DG ? vp[j]
+                  : (uint32_t)(qrow + 8 * j) * (uint32_t)ldQ + (uint32_t)(qc0 ^ (16 * j));
     }
-    to_lds4(ss, scale0 + buf, psc_off);
+    if (tail || (DG && outP < C::BP)) {
+      // columns past the end hold the next row's bytes: out of range instead
+      const int lim = DG ? outP : pleft;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        vp[j] = (pc0 ^ pxor(j)) < lim ? vp[j] : kOOB;
+        vq[j] = ((DG ? qc0 : pc0) ^ (16 * j)) < pleft ? vq[j] : kOOB;
+      }
+      // DGRAD's rows past the reduction's end
+      if (DG && tail)
+        rp.z = __builtin_amdgcn_readfirstlane((pleft - 1) * ldP + outP);
+    }
+    load_stage(rp, rq, rs, lp, lq, ls, vp, vq, vs);
     ++produced;
-    if (++pkt == nk) next_tile();
+    pbuf = pbuf == (uint32_t)((C::ST - 1) * C::STAGE) ? 0u : pbuf + (uint32_t)C::STAGE;
+    pleft -= kBlk;
+    if (pleft <= 0) {
+      next_tile();
+    } else {
+      advance(rp, stepP);
+      advance(rq, kBlk);
+      advance(rs, stepS);
+    }
   };
 
   // ---- consumer: fragment addresses.  Lane l of a fragment holds row l % 16
@@ -334,12 +434,10 @@ __global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
     const i32x4 hi = *reinterpret_cast<const i32x4*>(base + (off ^ 16u));
     return (i32x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto readQ = [&](int g, int j) {
-    const char* st = lds + (g % C::ST) * C::STAGE;
+  auto readQ = [&](const char* st, int j) {
     return frag(st + j * 2048, offQ ^ (uint32_t)(32 * (j & 1)));
   };
-  auto readP = [&](int g, int i) {
-    const char* st = lds + (g % C::ST) * C::STAGE;
+  auto readP = [&](const char* st, int i) {
     if constexpr (DG) {
       typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
       const uint32_t o = offT ^ (uint32_t)(16 * i);
@@ -356,18 +454,16 @@ __global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
       return frag(st + i * 2048, offP ^ (uint32_t)(32 * (i & 1)));
     }
   };
-  static_assert(C::MQ % 2 == 0, "swizzle parity");
-
   f32x4 acc[C::MP][C::MQ];
 #pragma unroll
   for (int i = 0; i < C::MP; ++i)
 #pragma unroll
     for (int j = 0; j < C::MQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  i32x8 fp[4], fq[C::MQ];
+  i32x8 fp[C::RING], fq[C::MQ];
   float rawq[C::MQ], raww;
-  auto read_scales = [&](int g) {
-    const float* sc = reinterpret_cast<const float*>(lds + (g % C::ST) * C::STAGE + C::DATA);
+  auto read_scales = [&](const char* st) {
+    const float* sc = reinterpret_cast<const float*>(st + C::DATA);
 #pragma unroll
     for (int j = 0; j < C::MQ; ++j) rawq[j] = sc[wq * C::WTQ + 16 * j + l16];
     raww = sc[C::BQ + wp * C::WTP / kBlk];
@@ -398,52 +494,84 @@ __global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
 
   next_tile();
 #pragma unroll
-  for (int s = 0; s < C::ST; ++s) produce();
-  Walk cw;
-  cw.init(total);
-  auto first_reads = [&](int g) {
-    read_scales(g);
-    fp[0] = readP(g, 0);
-    fp[1] = readP(g, 1);
-  };
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  for (int i = 0; i < C::ST; ++i) produce();
+  if (produced >= C::ST) wait_vmcnt<(C::ST - 1) * C::LOADS>();
+  else wait_vmcnt<0>();
   __syncthreads();
-  if (produced > 0) {
-    first_reads(0);
+  int g = 0;                                   // stages consumed
+  uint32_t cbuf = 0;                           // and the buffer of the current one
+  // The first reads of the stage in cbuf.
+  auto first_reads = [&]() {
+    read_scales(lds + cbuf);
+    fp[0] = readP(lds + cbuf, 0);
+    if (C::AHEAD == 2) fp[1] = readP(lds + cbuf, 1);
 #pragma unroll
-    for (int j = 0; j < C::MQ; ++j) fq[j] = readQ(0, j);
-  }
-  int g = 0;
-  for (; cw.at < cw.end; cw.at += cw.step) {
-    const Tile t = tile_of<C::BP, C::BQ>(cw.at, X, tilesP, gm);
-    for (int kt = 0; kt < nk; ++kt, ++g) {
+    for (int j = 0; j < C::MQ; ++j) fq[j] = readQ(lds + cbuf, j);
+  };
+  // On to the next stage: the current one is in registers and the next has
+  // landed; one barrier frees the one buffer and publishes the other.  (Behind
+  // the launch's last stage the reads fetch values that nothing uses.)
+  auto next_stage = [&]() {
+    if (g + C::ST <= produced) wait_vmcnt<(C::ST - 2) * C::LOADS>();
+    else wait_vmcnt<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    produce();
+    ++g;
+    cbuf = cbuf == (uint32_t)((C::ST - 1) * C::STAGE) ? 0u : cbuf + (uint32_t)C::STAGE;
+  };
+  first_reads();
+  while (nahead > 0) {
+    const Tile t = ahead[0];
+#pragma unroll
+    for (int u = 0; u < C::ST; ++u) ahead[u] = ahead[u + 1];
+    --nahead;
+    if (nk == 0) next_tile();                  // nothing to load: zeros are stored
+    // a wave none of whose rows exist takes part in the loads only: a tile of
+    // half the rows leaves the matrix cores to the other half's waves
+    const bool rows = __builtin_amdgcn_readfirstlane(t.q0 + wq * C::WTQ < t.q_end);
+    if (!rows) {
+      for (int kt = 0; kt < nk; ++kt) next_stage();
+      first_reads();
+      continue;
+    }
+    for (int kt = 0; kt < nk; ++kt) {
       float s[C::MQ];
 #pragma unroll
       for (int j = 0; j < C::MQ; ++j) s[j] = rawq[j] * raww;
-      f32x4 part[C::MQ];
+      f32x4 part[2][C::MQ];
+      // result block (i, j) of the stage into its accumulator.  The empty use
+      // pins it here: a product has no side effects, and the compiler would
+      // else move whole rows of them behind the waits and the barrier below,
+      // with every fragment held in registers until then.
+      auto add = [&](int i, int j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], s[j], acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));
+      };
+      const char* st = lds + cbuf;
 #pragma unroll
       for (int i = 0; i < C::MP; ++i) {
-        if (i + 2 < C::MP) fp[(i + 2) & 3] = readP(g, i + 2);
         const bool last = i == C::MP - 1;
+        if (i + C::AHEAD < C::MP) fp[(i + C::AHEAD) % C::RING] = readP(st, i + C::AHEAD);
+        __builtin_amdgcn_sched_barrier(0);           // (the read stays ahead of the products)
         if (last) {
-          // stage g is in registers and stage g + 1 has landed: one barrier
-          // frees the one buffer and publishes the other
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-          __syncthreads();
-          produce();
-          first_reads(g + 1);          // (of the launch's last stage: unused values)
+          next_stage();
+          read_scales(lds + cbuf);
+          fp[0] = readP(lds + cbuf, 0);
+          if (C::AHEAD == 2) fp[1] = readP(lds + cbuf, 1);
         }
 #pragma unroll
         for (int j = 0; j < C::MQ; ++j) {
-          part[j] = product(fp[i & 3], fq[j]);
-          if (last) fq[j] = readQ(g + 1, j);
+          part[i & 1][j] = product(fp[i % C::RING], fq[j]);
+          if (last) fq[j] = readQ(lds + cbuf, j);
+          if (i > 0) add(i - 1, j);
         }
-#pragma unroll
-        for (int j = 0; j < C::MQ; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], s[j], acc[i][j][e]);
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int j = 0; j < C::MQ; ++j) add(C::MP - 1, j);
     }
     store(t);
 #pragma unroll
@@ -451,63 +579,67 @@ __global__ __launch_bounds__(C::NT) void fp8_gemm_kernel(Fp8Args a) {
 #pragma unroll
       for (int j = 0; j < C::MQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_vmcnt<0>();
 }
 
 // ------------------------------------------------------------ few-row kernel --
 
-// FWD where experts have few rows: the weights are read once and nothing is
-// reused, so there is no LDS staging.  A workgroup of four waves computes 32
-// P indices x 32 rows; the waves take every fourth scale block, each loading
-// its fragments straight into registers (16 rows x 128 contiguous bytes per
-// fragment), four blocks in flight, and their fp32 sums meet in LDS in wave
-// order.
-constexpr int kFewP = 32, kFewQ = 32, kFewU = 4;
+// FWD where experts have few rows: a weight fragment meets one or two row
+// blocks, so there is no LDS staging.  A workgroup of NW waves computes 16 PB
+// P indices x 32 rows; the waves take every NW-th scale block, each loading its
+// fragments straight into registers (16 rows x 128 contiguous bytes per
+// fragment), U blocks in flight, and their fp32 sums meet in LDS in wave order.
+constexpr int kFewQ = 32;
 
-__global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Args a) {
+template <int PB, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8Args a) {
+  constexpr int P = 16 * PB;
+  static_assert(128 % P == 0, "one weight scale per tile and block");
   __shared__ int sched[2 * (kMaxExperts + 1)];
-  __shared__ __attribute__((aligned(16))) f32x4 sums[4][4][64];
+  __shared__ __attribute__((aligned(16))) f32x4 sums[NW][2 * PB][64];
   const int N = (int)a.N, K = (int)a.K;
   const int nk = (K + kBlk - 1) / kBlk, nn = (N + kBlk - 1) / kBlk;
-  const int tilesP = (N + kFewP - 1) / kFewP;
+  const int tilesP = (N + P - 1) / P;
   Experts X{sched, sched + kMaxExperts + 1, a.E, 0};
   setup_experts<kFewQ>(a.offsets, (int)a.M, X);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  Walk w;
-  for (w.init(X.mtiles * tilesP); w.at < w.end; w.at += w.step) {
-    const Tile t = tile_of<kFewP, kFewQ>(w.at, X, tilesP, 1 << 20);
-    const int rows = min(t.q_end - t.q0, kFewQ), cols = min(N - t.p0, kFewP);
+  Items<P, kFewQ, false> items;
+  items.init(X.mtiles * tilesP, tilesP, max(X.mtiles, 1));
+  Tile t = {0, 0, 0, 0};
+  while (items.next(X, tilesP, max(X.mtiles, 1), t)) {
+    const int rows = min(t.q_end - t.q0, kFewQ), cols = min(N - t.p0, P);
     const bool two = rows > 16;
-    const i32x4 rw = rsrc_of(static_cast<const uint8_t*>(a.w8) + ((int64_t)t.e * N + t.p0) * K,
-                             (uint32_t)cols * (uint32_t)K);
-    const i32x4 rx = rsrc_of(static_cast<const uint8_t*>(a.q8) + (int64_t)t.q0 * K,
-                             (uint32_t)rows * (uint32_t)K);
+    const auto rw = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(a.w8)) + ((int64_t)t.e * N + t.p0) * K,
+        (short)0, cols * K, 0x00020000);
+    const auto rx = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(a.q8)) + (int64_t)t.q0 * K, (short)0,
+        rows * K, 0x00020000);
     const float* wsc = a.ws + ((int64_t)t.e * nn + t.p0 / kBlk) * nk;
-    f32x4 acc[2][2];
+    f32x4 acc[PB][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto frag = [&](const i32x4& rs, int row, int kb) {
+    for (int i = 0; i < PB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // 32 bytes of row `row`, zeros past the reduction's end or the valid rows
+    auto frag = [&](auto rs, int row, int kb) {
       const uint32_t col = (uint32_t)(kb * kBlk + 32 * g4);
       const uint32_t off = (uint32_t)row * (uint32_t)K + col;
-      const auto d = __builtin_amdgcn_make_buffer_rsrc(
-          reinterpret_cast<void*>(((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x), (short)0, rs.z, rs.w);
       const i32x4 lo = __builtin_bit_cast(
-          i32x4, __builtin_amdgcn_raw_buffer_load_b128(d, (int)(off | (col < (uint32_t)K ? 0u : kOOB)), 0, 0));
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off | (col < (uint32_t)K ? 0u : kOOB)), 0, 0));
       const i32x4 hi = __builtin_bit_cast(
           i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                     d, (int)((off + 16u) | (col + 16u < (uint32_t)K ? 0u : kOOB)), 0, 0));
+                     rs, (int)((off + 16u) | (col + 16u < (uint32_t)K ? 0u : kOOB)), 0, 0));
       return (i32x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    for (int k0 = wave; k0 < nk; k0 += 4 * kFewU) {
-      i32x8 fw[kFewU][2], fx[kFewU][2];
-      float s[kFewU][2];
+    for (int k0 = wave; k0 < nk; k0 += NW * U) {
+      i32x8 fw[U][PB], fx[U][2];
+      float s[U][2];
 #pragma unroll
-      for (int u = 0; u < kFewU; ++u) {
-        const int kb = k0 + 4 * u;                   // past nk: the loads read zeros
-        fw[u][0] = frag(rw, l16, kb);
-        fw[u][1] = frag(rw, 16 + l16, kb);
+      for (int u = 0; u < U; ++u) {
+        const int kb = k0 + NW * u;                  // past nk: the loads read zeros
+#pragma unroll
+        for (int i = 0; i < PB; ++i) fw[u][i] = frag(rw, 16 * i + l16, kb);
         fx[u][0] = frag(rx, l16, kb);
         if (two) fx[u][1] = frag(rx, 16 + l16, kb);
         const bool in = kb < nk;
@@ -517,16 +649,16 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Args a) {
         s[u][1] = in && 16 + l16 < rows ? xs[16 + l16] * sw : 0.f;
       }
 #pragma unroll
-      for (int u = 0; u < kFewU; ++u) {
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < PB; ++i) {
           const f32x4 p = product(fw[u][i], fx[u][0]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][0][e] = __builtin_fmaf(p[e], s[u][0], acc[i][0][e]);
         }
         if (two) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < PB; ++i) {
             const f32x4 p = product(fw[u][i], fx[u][1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][1][e] = __builtin_fmaf(p[e], s[u][1], acc[i][1][e]);
@@ -536,17 +668,20 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Args a) {
     }
     __syncthreads();                                 // the previous tile's sums are read
 #pragma unroll
-    for (int b = 0; b < 4; ++b) sums[wave][b][lane] = acc[b >> 1][b & 1];
+    for (int i = 0; i < PB; ++i) {
+      sums[wave][2 * i][lane] = acc[i][0];
+      sums[wave][2 * i + 1][lane] = acc[i][1];
+    }
     __syncthreads();
-    // wave b finishes result block b
-    const int i = wave >> 1, j = wave & 1;
-    f32x4 r = sums[0][wave][lane];
+    for (int b = wave; b < 2 * PB; b += NW) {        // a wave finishes result block b
+      f32x4 r = sums[0][b][lane];
 #pragma unroll
-    for (int v = 1; v < 4; ++v) r += sums[v][wave][lane];
-    const int m = 16 * j + l16, n = t.p0 + 16 * i + 4 * g4;
-    if (m < rows && n < N)
-      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(t.q0 + m) * N + n) =
-          u32x2{pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3])};
+      for (int v = 1; v < NW; ++v) r += sums[v][b][lane];
+      const int m = 16 * (b & 1) + l16, n = t.p0 + 16 * (b >> 1) + 4 * g4;
+      if (m < rows && n < N)
+        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(t.q0 + m) * N + n) =
+            u32x2{pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3])};
+    }
   }
 }
 
@@ -580,25 +715,68 @@ unsigned grid_of(int64_t tiles, int64_t cap) {
   return (unsigned)(g < cap ? g : cap);
 }
 
-using Cfg = Fp8Cfg<128, 128, 2, 2, 2>;
+// 256 x 256 tiles, one workgroup of 8 waves per compute unit, and 128 x 128
+// tiles, two workgroups of 4 waves.
+using Big = Fp8Cfg<256, 256, 2, 4, 2>;
+using Small = Fp8Cfg<128, 128, 2, 2, 2>;
+
+template <class C>
+void launch_tiled(bool dgrad, const Fp8Args& a, int64_t tiles, int64_t cap, hipStream_t s) {
+  // (twice the tiles: the last round's may be halved)
+  const dim3 g(grid_of(2 * tiles, cap)), b(C::NT);
+  if (dgrad) hipLaunchKernelGGL((fp8_gemm_kernel<true, C>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((fp8_gemm_kernel<false, C>), g, b, 0, s, a);
+}
 
 }  // namespace
 
 int launch_fp8(bool dgrad, const Fp8Args& a, int64_t max_m, hipStream_t s) {
   const int64_t pdim = dgrad ? a.K : a.N;
-  const int cus = device_cus();
-  // Few rows per expert: nothing of a weight tile is reused, and the kernel
-  // that reads it straight into registers has shorter start-up.  Measured
-  // (forward, N = 768, K = 2048, eight experts of one row each): 12 us against
-  // 19 us; at 8 rows for each of 64 experts (N = 1536): 44 us against 39 us.
-  if (!dgrad && a.M < 8 * (int64_t)a.E) {
-    const int64_t tiles = tile_bound(a, pdim, max_m, kFewP, kFewQ);
-    hipLaunchKernelGGL(fp8_few_rows_kernel, dim3(grid_of(tiles, 8 * cus)), dim3(256), 0, s, a);
-  } else {
-    const dim3 g(grid_of(tile_bound(a, pdim, max_m, Cfg::BP, Cfg::BQ), 2 * cus)), b(Cfg::NT);
-    if (dgrad) hipLaunchKernelGGL((fp8_gemm_kernel<true, Cfg>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((fp8_gemm_kernel<false, Cfg>), g, b, 0, s, a);
+  const int64_t cus = device_cus();
+  // Which kernel: by the number of tiles that the rows give if they spread
+  // evenly (the host does not see the offsets; every expert's last tile is
+  // half full on average).  Results do not depend on the spread, only speed.
+  const int64_t live = a.E < a.M ? a.E : a.M;
+  // Few rows: 16 PB x 32 tiles straight from memory.  A quarter of a
+  // workgroup's time on a 128 x 128 tile is instructions that its products do
+  // not hide, so with too few tiles to fill the chip, or too few rows to reuse
+  // a staged weight tile, this kernel is faster.  Measured (us, this / tiled):
+  // 8 experts, N = 768, K = 2048: 6.0 / 17 at 1 row each, 11 / 17 at 64, 22 /
+  // 17 at 128; N = 1408, K = 7168: 20 / 49 at 1 row, 46 / 49 at 64; 64 experts,
+  // N = 4096, K = 2048: 58 / 66 at 1, 95 / 99 at 4, 118 / 102 at 16 rows.
+  if (!dgrad) {
+    int64_t mt = a.M / kFewQ + live / 2;
+    if (mt < live) mt = live;
+    const int64_t t64 = mt * ((pdim + 63) / 64);
+    if (a.M < 8 * live || t64 <= 2 * cus) {
+      // eight waves per 32-column tile while there are few tiles (1 row for
+      // each of 8 experts, K = 7168: 20 us against 25), else four per 64
+      // columns, which reads the rows half as often (16 rows, N = 4096: 17
+      // against 20)
+      if (t64 <= cus)
+        hipLaunchKernelGGL((fp8_few_rows_kernel<2, 8, 2>),
+                           dim3(grid_of(tile_bound(a, pdim, max_m, 32, kFewQ), 4 * cus)), dim3(512), 0,
+                           s, a);
+      else
+        hipLaunchKernelGGL((fp8_few_rows_kernel<4, 4, 2>),
+                           dim3(grid_of(tile_bound(a, pdim, max_m, 64, kFewQ), 8 * cus)), dim3(256), 0,
+                           s, a);
+      return (int)hipGetLastError();
+    }
   }
+  // Tiled: rounds of tiles over the chip times a round's time, in units of a
+  // 128 x 128 stage with one workgroup per compute unit.  A full round of
+  // stages measured 1.9 us (256 x 256), 1.15 us (128 x 128, two workgroups per
+  // compute unit) and 0.75 us (one): at K = N = M = 8192 the large tile is 20%
+  // faster, with fewer tiles than compute units the small one up to 30%.
+  auto tiles = [&](int64_t b) { return (2 * a.M / b + live + 1) / 2 * ((pdim + b - 1) / b); };
+  const double tb = (double)tiles(256) / cus, ts = (double)tiles(128) / cus;
+  const double big = 1.9 * (tb <= 0.5 ? 0.6 : tb <= 1.0 ? 1.0 : tb + 0.3);
+  const double small = ts <= 1.0 ? 0.75 : 1.15 * (ts <= 2.0 ? 1.0 : ts / 2 + 0.25);
+  if (big <= small)
+    launch_tiled<Big>(dgrad, a, tile_bound(a, pdim, max_m, Big::BP, Big::BQ), cus, s);
+  else
+    launch_tiled<Small>(dgrad, a, tile_bound(a, pdim, max_m, Small::BP, Small::BQ), 2 * cus, s);
   return (int)hipGetLastError();
 }
 
