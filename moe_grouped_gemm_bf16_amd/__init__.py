@@ -30,8 +30,33 @@ __all__ = ["fwd", "dgrad", "wgrad", "wgrad_noalloc", "fwd_swiglu", "dgrad_swiglu
            "MgemmError", "status_str", "LIB"]
 
 
+# The current stream's handle without building a torch.cuda.Stream object (2 us
+# of a call's 12), where this torch has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+class _Here:
+    """The device context of tensors that are on the current device."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(dev: torch.device):
+    """torch.cuda.device(dev), or nothing where dev is current already."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _ptr(t: torch.Tensor | None) -> int:
@@ -86,7 +111,7 @@ def fwd(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, max_m_per_e: in
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
     _same_device(x.device, w=w, out=out)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = LIB.mgemm_fwd(x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                            M, N, K, E, int(max_m_per_e), _stream(x))
     check(st, "mgemm_fwd")
@@ -112,7 +137,7 @@ def dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, max_m_per_e:
         if tuple(out.shape) != (M, K):
             raise ValueError(f"out must be [{M}, {K}]")
     _same_device(dy.device, w=w, out=out)
-    with torch.cuda.device(dy.device):
+    with _on(dy.device):
         st = LIB.mgemm_dgrad(dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                              M, N, K, E, int(max_m_per_e), _stream(dy))
     check(st, "mgemm_dgrad")
@@ -158,7 +183,7 @@ def _wgrad(fn: str, dy, x, offsets, E, out, accumulate):
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dy.device, x=x, out=out)
-    with torch.cuda.device(dy.device):
+    with _on(dy.device):
         st = getattr(LIB, fn)(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                               M, N, K, E, 1 if accumulate else 0, _stream(dy))
     check(st, fn)
@@ -210,7 +235,7 @@ def fwd_swiglu(x: torch.Tensor, w13: torch.Tensor, offsets: torch.Tensor,
             raise ValueError(f"gu_out must be [{M}, {2 * I}]")
         guptr = gu_out.data_ptr()
     _same_device(x.device, w13=w13, out=out, gu_out=gu_out)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = LIB.mgemm_fwd_swiglu_gu(x.data_ptr(), gptr, w13.data_ptr(), offsets.data_ptr(),
                                      out.data_ptr(), guptr, M, T, I, K, E, int(max_m_per_e),
                                      _stream(x))
@@ -242,7 +267,7 @@ def dgrad_swiglu(dy: torch.Tensor, w2: torch.Tensor, gu: torch.Tensor, offsets: 
         if tuple(out.shape) != (M, 2 * I):
             raise ValueError(f"out must be [{M}, {2 * I}]")
     _same_device(dy.device, w2=w2, gu=gu, out=out)
-    with torch.cuda.device(dy.device):
+    with _on(dy.device):
         st = LIB.mgemm_dgrad_swiglu(dy.data_ptr(), w2.data_ptr(), gu.data_ptr(),
                                     offsets.data_ptr(), out.data_ptr(), M, N, I, E,
                                     int(max_m_per_e), _stream(dy))
@@ -289,7 +314,7 @@ def grouped_list_desc(desc: torch.Tensor, G: int) -> None:
     """mgemm_list on a device descriptor array (from list_descriptors)."""
     if desc.dtype != torch.uint8 or not desc.is_cuda or desc.numel() != 48 * G:
         raise ValueError("desc must be the device uint8 array of G descriptors")
-    with torch.cuda.device(desc.device):
+    with _on(desc.device):
         st = LIB.mgemm_list(desc.data_ptr(), int(G), _stream(desc))
     check(st, "mgemm_list")
 
@@ -327,7 +352,7 @@ def mx_scales_blocked(scales: torch.Tensor, out: torch.Tensor | None = None) -> 
         if tuple(out.shape) != shape:
             raise ValueError(f"out must be {shape}")
     _same_device(scales.device, out=out)
-    with torch.cuda.device(scales.device):
+    with _on(scales.device):
         st = LIB.mg_mx_scales_blocked(scales.data_ptr(), out.data_ptr(), rows, 32 * nb, batch,
                                       _stream(scales))
     check(st, "mg_mx_scales_blocked")
@@ -362,7 +387,7 @@ def fwd_mx(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scale: t
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
     _same_device(x8.device, x_scale=x_scale, w8=w8, w_scale=w_scale, out=out)
-    with torch.cuda.device(x8.device):
+    with _on(x8.device):
         st = LIB.mgemm_fwd_mx(x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
                               offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e),
                               _stream(x8))
@@ -418,7 +443,7 @@ def fp8_quantize(x: torch.Tensor, gather: torch.Tensor | None = None,
     E = _rows_offsets(offsets, x.device)
     out, scales = _codes_out(M, K, x.device, out, scales, (M,))
     _same_device(x.device, out=out, scales=scales)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = LIB.mg_fp8_quantize(x.data_ptr(), 1 if x.dtype == torch.float32 else 0, _ptr(gather),
                                  _ptr(offsets), out.data_ptr(), scales.data_ptr(), M, T, K, E,
                                  _stream(x))
@@ -437,7 +462,7 @@ def fp8_quantize_swiglu(gu: torch.Tensor, offsets: torch.Tensor | None = None,
     E = _rows_offsets(offsets, gu.device)
     out, scales = _codes_out(M, I2 // 2, gu.device, out, scales, (M,))
     _same_device(gu.device, out=out, scales=scales)
-    with torch.cuda.device(gu.device):
+    with _on(gu.device):
         st = LIB.mg_fp8_quantize_swiglu(gu.data_ptr(), _ptr(offsets), out.data_ptr(),
                                         scales.data_ptr(), M, I2 // 2, E, _stream(gu))
     check(st, "mg_fp8_quantize_swiglu")
@@ -467,7 +492,7 @@ def fp8_quantize_weights(w: torch.Tensor, out: torch.Tensor | None = None,
         if tuple(scales.shape) != shape:
             raise ValueError(f"scales must be {list(shape)}")
     _same_device(w.device, out=out, scales=scales)
-    with torch.cuda.device(w.device):
+    with _on(w.device):
         st = LIB.mg_fp8_quantize_weights(w.data_ptr(), 1 if w.dtype == torch.float32 else 0,
                                          out.data_ptr(), scales.data_ptr(), E, N, K, _stream(w))
     check(st, "mg_fp8_quantize_weights")
@@ -520,7 +545,7 @@ def _product_fp8(fn, dgrad, q8, q_scale, w8, w_scale, offsets, max_m_per_e, out)
         if tuple(out.shape) != (M, P):
             raise ValueError(f"out must be [{M}, {P}]")
     _same_device(q8.device, w8=w8, out=out, **{scale: q_scale, "w_scale": w_scale})
-    with torch.cuda.device(q8.device):
+    with _on(q8.device):
         st = getattr(LIB, fn)(q8.data_ptr(), q_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
                               offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e),
                               _stream(q8))
@@ -559,7 +584,7 @@ def wgrad_mx(dyt8: torch.Tensor, dyt_scale: torch.Tensor, xt8: torch.Tensor,
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dyt8.device, dyt_scale=dyt_scale, xt8=xt8, xt_scale=xt_scale, out=out)
-    with torch.cuda.device(dyt8.device):
+    with _on(dyt8.device):
         st = LIB.kgemm_wgrad_mx(dyt8.data_ptr(), dyt_scale.data_ptr(), xt8.data_ptr(),
                                 xt_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                                 M, N, K, E, 1 if accumulate else 0, _stream(dyt8))
@@ -600,7 +625,7 @@ def wgrad_mx_tm(dy8: torch.Tensor, dy_scale: torch.Tensor, x8: torch.Tensor,
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dy8.device, dy_scale=dy_scale, x8=x8, x_scale=x_scale, out=out)
-    with torch.cuda.device(dy8.device):
+    with _on(dy8.device):
         st = LIB.kgemm_wgrad_mx_tm(dy8.data_ptr(), dy_scale.data_ptr(), x8.data_ptr(),
                                    x_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                                    M, N, K, E, 1 if accumulate else 0, _stream(dy8))
@@ -633,7 +658,7 @@ def moe_combine(rows: torch.Tensor, token_rows: torch.Tensor,
         if tuple(out.shape) != (T, D):
             raise ValueError(f"out must be [{T}, {D}]")
     _same_device(rows.device, token_rows=token_rows, weights=weights, out=out)
-    with torch.cuda.device(rows.device):
+    with _on(rows.device):
         st = LIB.mg_moe_combine(rows.data_ptr(), token_rows.data_ptr(), wptr, out.data_ptr(),
                                 M, T, k, D, _stream(rows))
     check(st, "mg_moe_combine")
@@ -668,7 +693,7 @@ def moe_combine_bwd(dout: torch.Tensor, rows: torch.Tensor, token_rows: torch.Te
         if tuple(drows.shape) != (M, D):
             raise ValueError(f"drows must be [{M}, {D}]")
     _same_device(rows.device, dout=dout, token_rows=token_rows, weights=weights, drows=drows)
-    with torch.cuda.device(rows.device):
+    with _on(rows.device):
         st = LIB.mg_moe_combine_bwd(dout.data_ptr(), rows.data_ptr(), token_rows.data_ptr(),
                                     _ptr(weights), drows.data_ptr(), _ptr(dweights), M, T, k, D,
                                     _stream(rows))
@@ -726,17 +751,17 @@ def moe_route(logits: torch.Tensor, k: int, normalize: bool = True,
             raise ValueError(f"mask must have {T} entries, got {mask.numel()}")
         _same_device(logits.device, mask=mask)
     dev = logits.device
-    # one allocation per type: the outputs are slices of it
-    f = torch.empty(T * k + T + E + 2, dtype=torch.float32, device=dev)
+    # one allocation per type, the outputs (and the workspace) being parts of it
     words = LIB.mg_moe_route_workspace(T, E) // 4
-    i = torch.empty(3 * T * k + E + 1 + local + 1, dtype=torch.int32, device=dev)
-    work = torch.empty(words, dtype=torch.int32, device=dev)
-    weights, lse, prob_sum, loss = f.split([T * k, T, E, 2])
-    experts, gather, token_rows, counts, tokens, offsets = i.split([T * k, T * k, T * k, E, 1,
-                                                                    local + 1])
+    n = T * k
+    f = torch.empty(n + T + E + 2, dtype=torch.float32, device=dev)
+    i = torch.empty(3 * n + E + 2 + local + words, dtype=torch.int32, device=dev)
+    weights, lse, prob_sum, loss = f.split_with_sizes((n, T, E, 2))
+    experts, gather, token_rows, counts, tokens, offsets, work = i.split_with_sizes(
+        (n, n, n, E, 1, local + 1, words))
     r = Route(weights.view(T, k), experts.view(T, k), lse, counts, prob_sum, tokens, loss, offsets,
               gather, token_rows.view(T, k))
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = LIB.mg_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
                               _ptr(mask), T, E, k, 1 if normalize else 0, int(first), local,
                               r.weights.data_ptr(), r.experts.data_ptr(), r.lse.data_ptr(),
@@ -786,7 +811,7 @@ def moe_route_bwd(logits: torch.Tensor, weights: torch.Tensor, experts: torch.Te
             raise ValueError(f"out must be [{T}, {E}]")
     _same_device(logits.device, weights=weights, experts=experts, lse=lse, counts=counts,
                  tokens=tokens, dweights=dweights, dloss=dloss, out=out)
-    with torch.cuda.device(logits.device):
+    with _on(logits.device):
         st = LIB.mg_moe_route_bwd(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
                                   weights.data_ptr(), experts.data_ptr(), lse.data_ptr(),
                                   counts.data_ptr(), tokens.data_ptr(), _ptr(dweights), _ptr(dloss),
