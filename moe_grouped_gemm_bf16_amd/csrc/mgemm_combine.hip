@@ -82,7 +82,9 @@ int launch_moe_combine(const uint16_t* rows, const int32_t* token_rows, const fl
 // rows[r], r = token_rows[t, j], once, writes drows[r] = w dout[t] (one
 // rounding to bf16) and dweights[t, j] = <rows[r], dout[t]> (fp32, the lanes'
 // sums added in a fixed order).  HBM-bound; the k waves of a token sit in one
-// workgroup where k = 8, so dout[t] comes from HBM once.
+// workgroup where k = 8, so dout[t] comes from HBM once; the rows, read and
+// written once, bypass the caches' order of use (8192 x 8 rows of 2048: 119 us
+// without, 112 us with, 5.1 TB/s, the rate of a large copy).
 __global__ __launch_bounds__(512) void moe_combine_bwd_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ rows,
     const int32_t* __restrict__ token_rows, const float* __restrict__ weights,
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(512) void moe_combine_bwd_kernel(
       for (int64_t c = 8 * lane; c < D; c += 512) {
         const u32x4_c d = *reinterpret_cast<const u32x4_c*>(dp + c);
         u32x4_c v = {0u, 0u, 0u, 0u}, o;
-        if (dweights != nullptr) v = *reinterpret_cast<const u32x4_c*>(rows + r * D + c);
+        if (dweights != nullptr) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_c*>(rows + r * D + c));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float d0 = __builtin_bit_cast(float, d[q] << 16);
@@ -109,7 +111,7 @@ __global__ __launch_bounds__(512) void moe_combine_bwd_kernel(
           o[q] = __builtin_bit_cast(
               uint32_t, __builtin_convertvector((f32x2_c){w * d0, w * d1}, bf16x2_c));
         }
-        *reinterpret_cast<u32x4_c*>(drows + r * D + c) = o;
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4_c*>(drows + r * D + c));
       }
     }
     if (dweights != nullptr) {
