@@ -25,7 +25,8 @@
 // minimum instructions exchange two entries; every lane sorts its own, and
 // four rotations each merge two descending lists into the upper half (k rounds
 // of a maximum each took 44 us of T = 65536, E = 256, k = 8, this takes
-// MEASURED us).  More than 16 experts are taken in rounds.
+// 30 us; 32-bit keys, which do not hold fp32 logits whole, took no less).
+// More than 16 experts are taken in rounds.
 //
 // The order is a counting sort in three launches: the token pass writes each
 // workgroup's counts, probability sums, lse^2 sum and n; a scan over the
@@ -852,7 +853,7 @@ int launch_tokens(RouteArgs a, hipStream_t s) {
   a.per_group = groups == 1 ? (a.T > 0 ? a.T : 1) : ((a.T + groups - 1) / groups + 63) / 64 * 64;
   if (groups == 1) {
     // few tokens: a quarter of the waves, which is what their barriers cost
-    // (T = 16, E = 128, k = 8: SMALL us against 12)
+    // (T = 16, E = 128, k = 8: 6.5 us against 12)
     if constexpr (L == 16) {
       if (a.T <= 64) {
         hipLaunchKernelGGL((route_tokens_kernel<T, L, V, KL, kSmallNT, true>), dim3(1),
