@@ -163,13 +163,13 @@ mg_status mg_moe_combine(const void* rows, const int32_t* token_rows, const floa
  *   dweights[t, j] = sum_d rows[r, d] dout[t, d]       (0 where there is no row)
  * dout: bf16 [T, D]; rows: bf16 [M, D] (read only for dweights; may be NULL
  * without it); weights: fp32 [T, k] or NULL (all 1); drows: bf16 [M, D]
- * (written, one rounding; rows that no entry names are left as they were);
- * dweights: fp32 [T, k] (written) or NULL.  Every row index may occur once in
- * token_rows, as mg_moe_route makes it (checked only under MGEMM_VALIDATE=1:
- * of a row named twice one of the two gradients would remain).  fp32
- * arithmetic, bitwise reproducible.  D a multiple of 8, 1 <= k <= 64; dout,
- * rows and drows 16-byte aligned.  T == 0 is a no-op; D == 0 or M == 0 writes
- * zero dweights.  Allocates nothing. */
+ * (written, one rounding; rows that no entry names are left as they were; must
+ * not overlap the inputs); dweights: fp32 [T, k] (written) or NULL.  Every row
+ * index may occur once in token_rows, as mg_moe_route makes it (checked only
+ * under MGEMM_VALIDATE=1: of a row named twice one of the two gradients would
+ * remain).  fp32 arithmetic, bitwise reproducible.  D a multiple of 8,
+ * 1 <= k <= 64; dout, rows and drows 16-byte aligned.  T == 0 is a no-op; D == 0
+ * or M == 0 writes zero dweights.  Allocates nothing. */
 mg_status mg_moe_combine_bwd(const void* dout, const void* rows, const int32_t* token_rows,
                              const float* weights, void* drows, float* dweights, int64_t M,
                              int64_t T, int32_t k, int64_t D, void* stream);
@@ -362,8 +362,8 @@ mg_status mg_fp8_quantize_swiglu(const void* gu, const int32_t* offsets, void* c
 /* Weights to block-scaled fp8, one scale per 128 x 128 block (of an expert;
  * edge blocks are smaller), by the rule of mg_fp8_quantize: w: bf16 or fp32
  * [E, N, K]; codes: uint8 [E, N, K]; scales: fp32 [E, ceil(N/128),
- * ceil(K/128)].  K a multiple of 16.  Empty sizes are a no-op.  Allocates
- * nothing. */
+ * ceil(K/128)].  K a multiple of 16; fewer than 2^24 blocks.  Empty sizes are
+ * a no-op.  Allocates nothing. */
 mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, float* scales,
                                   int64_t E, int64_t N, int64_t K, void* stream);
 

@@ -79,12 +79,16 @@ mg_status maybe_validate_rows(const int32_t* token_rows, int64_t n, int64_t M, h
     return v != nullptr && v[0] == '1';
   }();
   if (!on) return MG_OK;
-  std::vector<int32_t> h(static_cast<size_t>(n));
-  if (hipMemcpyAsync(h.data(), token_rows, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, s) !=
-          hipSuccess ||
-      hipStreamSynchronize(s) != hipSuccess)
-    return MG_ERR_DEVICE;
-  return mg_check_rows_host(h.data(), n, M);
+  try {
+    std::vector<int32_t> h(static_cast<size_t>(n));
+    if (hipMemcpyAsync(h.data(), token_rows, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost,
+                       s) != hipSuccess ||
+        hipStreamSynchronize(s) != hipSuccess)
+      return MG_ERR_DEVICE;
+    return mg_check_rows_host(h.data(), n, M);
+  } catch (...) {
+    return MG_ERR_DEVICE;                            // out of host memory
+  }
 }
 
 static_assert(sizeof(mg_gemm_desc) == sizeof(mg::ListDesc) &&
@@ -422,7 +426,8 @@ mg_status mg_moe_combine_bwd(const void* dout, const void* rows, const int32_t* 
 namespace {
 
 mg_status check_route(int64_t T, int32_t E, int32_t k) {
-  if (E < 1 || E > mg::kMaxExperts || k < 1 || k > 64 || k > E || T < 0 || T * k > kMaxRows)
+  if (E < 1 || E > mg::kMaxExperts || k < 1 || k > 64 || k > E || T < 0 || T > kMaxRows ||
+      T * k > kMaxRows)
     return MG_ERR_SHAPE;
   return MG_OK;
 }
@@ -432,7 +437,7 @@ bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 }  // namespace
 
 int64_t mg_moe_route_workspace(int64_t T, int32_t E) {
-  return T < 0 || E < 1 || E > mg::kMaxExperts ? 0 : mg::route_workspace_bytes(T, E);
+  return T < 0 || T > kMaxRows || E < 1 || E > mg::kMaxExperts ? 0 : mg::route_workspace_bytes(T, E);
 }
 
 mg_status mg_moe_route(const void* logits, int32_t logits_bf16, const uint8_t* mask, int64_t T,
@@ -544,8 +549,8 @@ mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, fl
                                   int64_t E, int64_t N, int64_t K, void* stream) {
   if (E < 0 || N < 0 || K < 0 || E > kMaxRows || N > kMaxDim || K > kMaxDim || (K & 15))
     return MG_ERR_SHAPE;
-  if (E * ((N + 127) / 128) > kMaxRows ||
-      E * ((N + 127) / 128) * ((K + 127) / 128) > kMaxRows)
+  if (E * ((N + 127) / 128) > mg::kMaxBlocks256 ||
+      E * ((N + 127) / 128) * ((K + 127) / 128) > mg::kMaxBlocks256)
     return MG_ERR_SHAPE;
   if (E == 0 || N == 0 || K == 0) return MG_OK;
   if (!w || !codes || !scales) return MG_ERR_NULL;

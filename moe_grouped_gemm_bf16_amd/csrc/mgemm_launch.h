@@ -12,6 +12,10 @@ enum { kFwd = 0, kDgrad = 1, kWgrad = 2, kFwdSwiglu = 3, kList = 4, kFwdMx = 5, 
 // per-expert tile prefix in LDS, two entries per thread of a 512-thread block.
 constexpr int kMaxExperts = 1024;
 
+// Most workgroups of 256 threads in one grid dimension: a dimension holds less
+// than 2^32 threads.
+constexpr int64_t kMaxBlocks256 = (int64_t(1) << 24) - 1;
+
 // One group of the descriptor-list call (same layout as mg_gemm_desc of the
 // C ABI): D [m, n] = A [m, k] B [n, k]^T, row strides in elements.
 struct ListDesc {

@@ -101,13 +101,24 @@ __device__ __forceinline__ u32x2 encode8(const float (&f)[8], float inv) {
   return u32x2{w[0], w[1]};
 }
 
+// Workgroup -> item, in runs of `run` neighbouring items: workgroup b runs on
+// XCD b % 8, and a run (the pieces of the same rows) stays on one, whose cache
+// then holds whole lines where a piece's codes end inside a 128-byte line.
+// What is left behind the last eight runs is taken in order.
+__device__ __forceinline__ uint32_t in_runs(uint32_t b, uint32_t blocks, uint32_t run) {
+  const uint32_t runs = blocks / run & ~7u, at = b >> 3;
+  return b < runs * run ? ((at / run) * 8 + (b & 7)) * run + at % run : b;
+}
+
 // Rows: a workgroup takes 4 RW rows x 4 blocks; wave w rows RW w .. + RW - 1,
 // its four lane rows the four blocks.  SWI: x holds g | u of 2 K columns and
 // the value is silu(g) u.  Workgroups go along the columns first: the pieces
 // of a row that are in flight together are neighbours in memory (32768 x 4096
 // bf16: 98 us with the rows first, 73 us so; 66 us with streaming reads, which
 // gathered rows, read again for every expert, do not get; 61 us with two rows
-// per wave in place of eight: 6.7 TB/s).
+// per wave in place of eight: 6.7 TB/s).  Where K is no multiple of 128 codes'
+// lines are shared by pieces, and a row's pieces go to one XCD (16384 x 6832:
+// 79 us without, 65 us with; at K = 4096 gathered rows 58 and 65 us).
 constexpr int kBlocks = 4;
 
 template <typename T, bool SWI, bool GATHER>
@@ -117,7 +128,9 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8RowsArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int blk = lane >> 4;
   const int64_t nb = (a.K + 127) / 128;
-  const int64_t b0 = (int64_t)blockIdx.x * kBlocks;
+  const uint32_t gx = (uint32_t)((nb + kBlocks - 1) / kBlocks), gy = gridDim.x / gx;
+  const uint32_t item = in_runs(blockIdx.x, gridDim.x, a.K % 128 ? gx : 1);
+  const int64_t b0 = (int64_t)(item % gx) * kBlocks;
   const int64_t col = (b0 + blk) * 128 + 8 * (lane & 15);
   int64_t end = a.M;
   if (a.offsets != nullptr) {
@@ -126,7 +139,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8RowsArgs a) {
   }
   const T* x = static_cast<const T*>(a.x);
   const int64_t ld = SWI ? 2 * a.K : a.K;
-  for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < end; r0 += (int64_t)gridDim.y * kRows) {
+  for (int64_t r0 = (int64_t)(item / gx) * kRows; r0 < end; r0 += (int64_t)gy * kRows) {
     Eight<T> v[RW], u[SWI ? RW : 1];
     int64_t src[RW];                                   // the rows' places in x, -1 = zeros
 #pragma unroll
@@ -177,7 +190,9 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8RowsArgs a) {
 }
 
 // Weights: a workgroup takes one 128 x 128 block, 16 lanes per row, eight rows
-// per lane, and finds the block's maximum through LDS.
+// per lane, and finds the block's maximum through LDS; a row of blocks goes to
+// one XCD (fp32, 20 x 1808 x 6832: 358 us without, 269 us with, 4.6 TB/s;
+// 32 x 4096 x 2048: 251 and 234 us).
 template <typename T>
 __global__ __launch_bounds__(256) void fp8_weights_kernel(const T* __restrict__ w,
                                                           uint8_t* __restrict__ codes,
@@ -186,7 +201,8 @@ __global__ __launch_bounds__(256) void fp8_weights_kernel(const T* __restrict__ 
   __shared__ float part[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t nk = (K + 127) / 128, nn = (N + 127) / 128;
-  const int64_t kb = blockIdx.x % nk, en = blockIdx.x / nk;
+  const uint32_t item = in_runs(blockIdx.x, gridDim.x, (uint32_t)nk);
+  const int64_t kb = item % nk, en = item / nk;
   const int64_t e = en / nn, n0 = (en - e * nn) * 128;
   const int64_t col = kb * 128 + 8 * (lane & 15);
   Eight<T> v[8];
@@ -224,8 +240,9 @@ __global__ __launch_bounds__(256) void fp8_weights_kernel(const T* __restrict__ 
 int launch_fp8_rows(const Fp8RowsArgs& a, bool fp32, bool swiglu, hipStream_t s) {
   const int64_t gx = ((a.K + 127) / 128 + kBlocks - 1) / kBlocks;
   int64_t gy = (a.M + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave);
-  if (gy > 65535) gy = 65535;                           // grid-stride beyond
-  const dim3 g((unsigned)gx, (unsigned)gy), b(256);
+  const int64_t most = kMaxBlocks256 / gx;              // grid-stride beyond
+  if (gy > most) gy = most;
+  const dim3 g((unsigned)(gx * gy)), b(256);
   const bool gather = a.gather != nullptr;
   if (swiglu) hipLaunchKernelGGL((fp8_rows_kernel<uint16_t, true, false>), g, b, 0, s, a);
   else if (fp32 && gather) hipLaunchKernelGGL((fp8_rows_kernel<float, false, true>), g, b, 0, s, a);

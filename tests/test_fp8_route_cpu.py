@@ -139,6 +139,16 @@ def test_quantizer_argument_errors():
     assert h(None, 0, None, None, 2, 0, 32, None) == OK
 
 
+def test_sizes_past_the_grid():
+    h = L.mg_fp8_quantize_weights
+    assert h(A, 0, A, A, 1 << 24, 1, 16, None) == SHAPE
+    assert h(A, 0, A, A, 1 << 12, 1 << 12, 1 << 14, None) == SHAPE
+    assert h(None, 0, A, A, (1 << 24) - 1, 1, 16, None) == NUL            # the sizes alone are fine
+    # T k past 64 bits
+    assert L.mg_moe_route(*_route_args(T=1 << 58, E=64, k=64, local=64)) == SHAPE
+    assert L.mg_moe_route_workspace(2 ** 63 - 1, 64) == 0
+
+
 def _route_args(**kw):
     a = dict(logits=A, bf16=0, mask=None, T=8, E=16, k=2, normalize=1, first=0, local=16, weights=A, experts=A, lse=A, counts=A, prob_sum=A,
              tokens=A, loss=A, offsets=A, gather=A, token_rows=A, workspace=A, bytes=1 << 20, stream=None)
