@@ -79,6 +79,26 @@ __device__ __forceinline__ void load_stage(const i32x4& rp, const i32x4& rq, con
       : "memory", "scc");
 }
 
+// The same for eight pieces of one operand.
+__device__ __forceinline__ void load_block(const i32x4& r, uint32_t to, const uint32_t (&v)[8]) {
+  uint32_t save;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %8, %10, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %9, %10, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(save)
+      : "s"(to), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]),
+        "v"(v[7]), "s"(r)
+      : "memory", "scc");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -584,72 +604,130 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
 
 // ------------------------------------------------------------ few-row kernel --
 
-// FWD where experts have few rows: a weight fragment meets one or two row
-// blocks, so there is no LDS staging.  A workgroup of NW waves computes 16 PB
-// P indices x 32 rows; the waves take every NW-th scale block, each loading its
-// fragments straight into registers (16 rows x 128 contiguous bytes per
-// fragment), U blocks in flight, and their fp32 sums meet in LDS in wave order.
+// Where experts have few rows a weight fragment meets one or two row blocks, so
+// no tile is shared between waves.  A workgroup of NW waves computes 16 PB P
+// indices x 32 rows; the waves take every NW-th scale block, U blocks in
+// flight, and their fp32 sums meet in LDS in wave order.  FWD's fragments (16
+// rows x 128 contiguous bytes) come straight from memory into registers;
+// DGRAD's weights, whose steps lie in different rows, pass through a part of
+// LDS of the wave's own, from which they are read transposed.
 constexpr int kFewQ = 32;
 
-template <int PB, int NW, int U>
+template <bool DG, int PB, int NW, int U>
 __global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8Args a) {
   constexpr int P = 16 * PB;
   static_assert(128 % P == 0, "one weight scale per tile and block");
+  static_assert(!DG || PB == 4, "the weights' places in LDS");
+  constexpr int kBlock = kBlk * P;                   // DGRAD: one block's weights
+  constexpr int kSums = 2 * PB * 64 * 16, kOwn = DG && U * kBlock > kSums ? U * kBlock : kSums;
   __shared__ int sched[2 * (kMaxExperts + 1)];
-  __shared__ __attribute__((aligned(16))) f32x4 sums[NW][2 * PB][64];
-  const int N = (int)a.N, K = (int)a.K;
-  const int nk = (K + kBlk - 1) / kBlk, nn = (N + kBlk - 1) / kBlk;
-  const int tilesP = (N + P - 1) / P;
+  __shared__ __attribute__((aligned(16))) char own[NW][kOwn];
+  const int red = (int)(DG ? a.N : a.K), Pdim = (int)(DG ? a.K : a.N);
+  const int64_t ldw = a.K;
+  const int nk = (red + kBlk - 1) / kBlk, np = (Pdim + kBlk - 1) / kBlk;
+  const int tilesP = (Pdim + P - 1) / P;
   Experts X{sched, sched + kMaxExperts + 1, a.E, 0};
   setup_experts<kFewQ>(a.offsets, (int)a.M, X);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
+  // DGRAD: block u's 128 rows of 64 bytes, chunk c of row r at c ^ (r / 4 % 2)
+  // ^ (2 (r / 32 % 2)): the transpose reads of 8 rows by two lane groups, 32
+  // rows apart, hit 16 distinct 16-byte banks.  Piece j of a block is rows
+  // 16 j .. + 15, a lane's chunk being that of piece 0 with j / 2 % 2 in bit 1.
+  const int drow = lane >> 2, dcol = 16 * ((lane & 3) ^ ((drow >> 2) & 1));
+  const int trow = 32 * g4 + (l16 >> 1);
+  const uint32_t toff = (uint32_t)trow * P + 16u * (uint32_t)(2 * (g4 & 1) ^ ((trow >> 2) & 1)) +
+                        8u * (uint32_t)(l16 & 1);
   Items<P, kFewQ, false> items;
   items.init(X.mtiles * tilesP, tilesP, max(X.mtiles, 1));
   Tile t = {0, 0, 0, 0};
   while (items.next(X, tilesP, max(X.mtiles, 1), t)) {
-    const int rows = min(t.q_end - t.q0, kFewQ), cols = min(N - t.p0, P);
+    const int rows = min(t.q_end - t.q0, kFewQ), cols = min(Pdim - t.p0, P);
     const bool two = rows > 16;
+    const uint8_t* w = static_cast<const uint8_t*>(a.w8) + (int64_t)t.e * a.N * a.K;
     const auto rw = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(static_cast<const uint8_t*>(a.w8)) + ((int64_t)t.e * N + t.p0) * K,
-        (short)0, cols * K, 0x00020000);
+        const_cast<uint8_t*>(w + (DG ? 0 : (int64_t)t.p0 * ldw)), (short)0,
+        DG ? 0 : cols * (int)ldw, 0x00020000);
     const auto rx = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(static_cast<const uint8_t*>(a.q8)) + (int64_t)t.q0 * K, (short)0,
-        rows * K, 0x00020000);
-    const float* wsc = a.ws + ((int64_t)t.e * nn + t.p0 / kBlk) * nk;
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(a.q8)) + (int64_t)t.q0 * red, (short)0,
+        rows * red, 0x00020000);
+    // the weights' scale of block kb
+    const int64_t sblock = DG ? np : 1;
+    const float* wsc = a.ws + (DG ? (int64_t)t.e * nk * np + t.p0 / kBlk
+                                  : ((int64_t)t.e * np + t.p0 / kBlk) * nk);
     f32x4 acc[PB][2];
 #pragma unroll
     for (int i = 0; i < PB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
     // 32 bytes of row `row`, zeros past the reduction's end or the valid rows
     auto frag = [&](auto rs, int row, int kb) {
       const uint32_t col = (uint32_t)(kb * kBlk + 32 * g4);
-      const uint32_t off = (uint32_t)row * (uint32_t)K + col;
+      const uint32_t off = (uint32_t)row * (uint32_t)red + col;
       const i32x4 lo = __builtin_bit_cast(
-          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off | (col < (uint32_t)K ? 0u : kOOB)), 0, 0));
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off | (col < (uint32_t)red ? 0u : kOOB)), 0, 0));
       const i32x4 hi = __builtin_bit_cast(
           i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                     rs, (int)((off + 16u) | (col + 16u < (uint32_t)K ? 0u : kOOB)), 0, 0));
+                     rs, (int)((off + 16u) | (col + 16u < (uint32_t)red ? 0u : kOOB)), 0, 0));
+      return (i32x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // DGRAD: block kb's weights to the wave's LDS; rows and columns past their
+    // ends, and blocks past nk, are zeros
+    auto stage = [&](int u, int kb) {
+      const int left = min(red - kb * kBlk, kBlk);
+      const i32x4 rs = rsrc_of(w + (int64_t)(left > 0 ? kb : 0) * kBlk * ldw + t.p0,
+                               left > 0 ? (uint32_t)(left - 1) * (uint32_t)ldw + (uint32_t)cols : 0u);
+      const uint32_t to = lds_addr_of(own[wave]) + (uint32_t)(u * kBlock);
+      uint32_t off[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = dcol ^ (32 * ((j >> 1) & 1));
+        off[j] = c < cols ? (uint32_t)(16 * j + drow) * (uint32_t)ldw + (uint32_t)c : kOOB;
+      }
+      load_block(rs, to, off);
+    };
+    auto staged = [&](int u, int i) {
+      typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+      auto tr = [&](uint32_t off) {
+        return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (lds_i32x2*)((__attribute__((address_space(3))) char*)(
+                             (__attribute__((address_space(3))) void*)own[wave]) + u * kBlock + off));
+      };
+      // rows 8 further: r / 4 % 2 and r / 32 % 2 are the same
+      const uint32_t o = toff ^ (uint32_t)(16 * i);
+      const i32x2 a0 = tr(o), a1 = tr(o + 8 * P), a2 = tr(o + 16 * P), a3 = tr(o + 24 * P);
+      const i32x4 lo = __builtin_shufflevector(a0, a1, 0, 1, 2, 3);
+      const i32x4 hi = __builtin_shufflevector(a2, a3, 0, 1, 2, 3);
       return (i32x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     for (int k0 = wave; k0 < nk; k0 += NW * U) {
       i32x8 fw[U][PB], fx[U][2];
       float s[U][2];
+      // (the reads of the last round's blocks are done)
+      if constexpr (DG) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int kb = k0 + NW * u;                  // past nk: the loads read zeros
+        if constexpr (DG) {
+          stage(u, kb);
+        } else {
 #pragma unroll
-        for (int i = 0; i < PB; ++i) fw[u][i] = frag(rw, 16 * i + l16, kb);
+          for (int i = 0; i < PB; ++i) fw[u][i] = frag(rw, 16 * i + l16, kb);
+        }
         fx[u][0] = frag(rx, l16, kb);
         if (two) fx[u][1] = frag(rx, 16 + l16, kb);
         const bool in = kb < nk;
-        const float sw = in ? wsc[kb] : 0.f;
+        const float sw = in ? wsc[kb * sblock] : 0.f;
         const float* xs = a.qs + (int64_t)(in ? kb : 0) * a.M + t.q0;
         s[u][0] = in && l16 < rows ? xs[l16] * sw : 0.f;
         s[u][1] = in && 16 + l16 < rows ? xs[16 + l16] * sw : 0.f;
       }
+      if constexpr (DG) wait_vmcnt<0>();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if constexpr (DG) {
+#pragma unroll
+          for (int i = 0; i < PB; ++i) fw[u][i] = staged(u, i);
+        }
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
           const f32x4 p = product(fw[u][i], fx[u][0]);
@@ -666,22 +744,25 @@ __global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8Args a) {
         }
       }
     }
-    __syncthreads();                                 // the previous tile's sums are read
+    auto sums = [&](int v) { return reinterpret_cast<f32x4*>(own[v]); };
+    if constexpr (DG) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    else __syncthreads();                            // the previous tile's sums are read
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
-      sums[wave][2 * i][lane] = acc[i][0];
-      sums[wave][2 * i + 1][lane] = acc[i][1];
+      sums(wave)[(2 * i) * 64 + lane] = acc[i][0];
+      sums(wave)[(2 * i + 1) * 64 + lane] = acc[i][1];
     }
     __syncthreads();
     for (int b = wave; b < 2 * PB; b += NW) {        // a wave finishes result block b
-      f32x4 r = sums[0][b][lane];
+      f32x4 r = sums(0)[b * 64 + lane];
 #pragma unroll
-      for (int v = 1; v < NW; ++v) r += sums[v][b][lane];
+      for (int v = 1; v < NW; ++v) r += sums(v)[b * 64 + lane];
       const int m = 16 * (b & 1) + l16, n = t.p0 + 16 * (b >> 1) + 4 * g4;
-      if (m < rows && n < N)
-        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(t.q0 + m) * N + n) =
+      if (m < rows && n < Pdim)
+        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(t.q0 + m) * Pdim + n) =
             u32x2{pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3])};
     }
+    if constexpr (DG) __syncthreads();               // the sums are read, the next tile's loads may land
   }
 }
 
@@ -737,33 +818,34 @@ int launch_fp8(bool dgrad, const Fp8Args& a, int64_t max_m, hipStream_t s) {
   // evenly (the host does not see the offsets; every expert's last tile is
   // half full on average).  Results do not depend on the spread, only speed.
   const int64_t live = a.E < a.M ? a.E : a.M;
-  // Few rows: 16 PB x 32 tiles straight from memory.  A quarter of a
-  // workgroup's time on a 128 x 128 tile is instructions that its products do
-  // not hide, so with too few tiles to fill the chip, or too few rows to reuse
-  // a staged weight tile, this kernel is faster.  Measured (us, this / tiled):
-  // 8 experts, N = 768, K = 2048: 6.0 / 17 at 1 row each, 11 / 17 at 64, 22 /
-  // 17 at 128; N = 1408, K = 7168: 20 / 49 at 1 row, 46 / 49 at 64; 64 experts,
-  // N = 4096, K = 2048: 58 / 66 at 1, 95 / 99 at 4, 118 / 102 at 16 rows.
-  if (!dgrad) {
-    int64_t mt = a.M / kFewQ + live / 2;
-    if (mt < live) mt = live;
-    const int64_t t64 = mt * ((pdim + 63) / 64);
-    if (a.M < 8 * live || t64 <= 2 * cus) {
-      // eight waves per 32-column tile while there are few tiles (1 row for
-      // each of 8 experts, K = 7168: 20 us against 25), else four per 64
-      // columns, which reads the rows half as often (16 rows, N = 4096: 17
-      // against 20)
-      if (t64 <= cus)
-        hipLaunchKernelGGL((fp8_few_rows_kernel<2, 8, 2>),
-                           dim3(grid_of(tile_bound(a, pdim, max_m, 32, kFewQ), 4 * cus)), dim3(512), 0,
-                           s, a);
-      else
-        hipLaunchKernelGGL((fp8_few_rows_kernel<4, 4, 2>),
-                           dim3(grid_of(tile_bound(a, pdim, max_m, 64, kFewQ), 8 * cus)), dim3(256), 0,
-                           s, a);
-      return (int)hipGetLastError();
-    }
-  }
+  // Few rows: tiles of 32 rows.  With too few 128 x 128 tiles to fill the chip,
+  // or too few rows to reuse a staged weight tile, a round of those is bound by
+  // what its products do not hide, and this kernel is faster.  Measured (us,
+  // this / tiled), FWD: 8 experts, N = 768, K = 2048: 6.0 / 17 at 1 row each,
+  // 11 / 17 at 64, 22 / 17 at 128; N = 1408, K = 7168: 20 / 49 at 1 row, 46 / 49
+  // at 64; 64 experts, N = 4096, K = 2048: 58 / 66 at 1, 95 / 99 at 4, 118 / 102
+  // at 16 rows.  DGRAD: 3 experts, N = 3520, K = 2288: 10 / 30 at 1 row each,
+  // 18 / 31 at 128; 16 experts: 29 / 34 at 16, 33 / 34 at 32, 47 / 41 at 64;
+  // 64 experts, N = 416, K = 5904: 42 / 45 at 16, 51 / 45 at 32.
+  int64_t mt = a.M / kFewQ + live / 2;
+  if (mt < live) mt = live;
+  const int64_t t64 = mt * ((pdim + 63) / 64);
+  auto few = [&](auto kernel, int p, int nw, int64_t cap) {
+    hipLaunchKernelGGL(kernel, dim3(grid_of(tile_bound(a, pdim, max_m, p, kFewQ), cap * cus)),
+                       dim3(64 * nw), 0, s, a);
+    return (int)hipGetLastError();
+  };
+  if (dgrad && (a.M <= 16 * live || t64 <= 4 * cus))
+    // (16 experts, N = 768, K = 2048, 32 rows each: 9 us, with two blocks in
+    // flight 12, LDS then holding one workgroup; 3 experts, N = 3520, K = 2288, 1
+    // row: 10 us, with four waves 12)
+    return few(fp8_few_rows_kernel<true, 4, 8, 1>, 64, 8, 4);
+  if (!dgrad && (a.M < 8 * live || t64 <= 2 * cus))
+    // eight waves per 32-column tile while there are few tiles (1 row for each
+    // of 8 experts, K = 7168: 20 us against 25), else four per 64 columns, which
+    // reads the rows half as often (16 rows, N = 4096: 17 against 20)
+    return t64 <= cus ? few(fp8_few_rows_kernel<false, 2, 8, 2>, 32, 8, 4)
+                      : few(fp8_few_rows_kernel<false, 4, 4, 2>, 64, 4, 8);
   // Tiled: rounds of tiles over the chip times a round's time, in units of a
   // 128 x 128 stage with one workgroup per compute unit.  A full round of
   // stages measured 1.9 us (256 x 256), 1.15 us (128 x 128, two workgroups per

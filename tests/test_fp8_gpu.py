@@ -209,6 +209,120 @@ def test_two_streams_and_a_replayed_graph_give_the_eager_bits():
             assert torch.equal(o, run(d, a)), i
 
 
+# -- the tiled forms: enough 64-column pieces that the few-row form is not taken -----
+
+# rows per expert, output width, reduction; from 4000 rows on in the large tiles
+TILED = [
+    ([300], 8208, 144), ([127, 128, 129, 0, 1], 8208, 400), ([257, 40], 8400, 1536), ([33, 64, 2, 0, 0, 95], 8208, 720),
+    ([200, 0, 184, 128], 8192, 16), ([4097], 8208, 144), ([2100, 0, 1877, 3], 8208, 272), ([1500, 0, 3000, 70, 1], 8336, 1040),
+]
+
+
+def _random_operands(sizes, P, R, dgrad, seed, extra=0):
+    """Random codes and scales as device tensors: (q, s, w8, ws, off)."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    N, K = (R, P) if dgrad else (P, R)
+    M, E, d = sum(sizes) + extra, len(sizes), dict(device="cuda", generator=g)
+    code = lambda *shape: torch.randint(0, 120, shape, dtype=torch.uint8, **d) | (torch.randint(0, 2, shape, dtype=torch.uint8, **d) << 7)  # noqa: E731
+    scale = lambda *shape: torch.rand(shape, **d) + 0.5                                                                                 # noqa: E731
+    return code(M, R), scale(-(-R // 128), M), code(E, N, K), scale(E, -(-N // 128), -(-K // 128)), torch.from_numpy(_offsets(sizes)).cuda()
+
+
+def _exact_on_device(q, s, w8, ws, off, dgrad):
+    """Exact sums and sums of the magnitudes, fp64."""
+    table = torch.from_numpy(ref.e4m3_values()).cuda()
+    R, N, K = q.shape[1], w8.shape[1], w8.shape[2]
+    x = table[q.int()] * s.t().double().repeat_interleave(128, 1)[:, :R]
+    out = [torch.zeros(q.shape[0], K if dgrad else N, dtype=torch.float64, device="cuda") for _ in range(2)]
+    off = off.tolist()
+    for e in range(len(off) - 1):
+        w = table[w8[e].int()] * ws[e].double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        w = w if dgrad else w.t().contiguous()
+        rows = slice(off[e], off[e + 1])
+        out[0][rows], out[1][rows] = x[rows] @ w, x[rows].abs() @ w.abs()
+    return out
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("i", range(len(TILED)))
+def test_tiled_product_against_exact_sums(i, dgrad):
+    sizes, P, R = TILED[i]
+    _say("tiled", sizes, P, R, "dgrad" if dgrad else "fwd")
+    ops = _random_operands(sizes, P, R, dgrad, 200 + i, extra=5)
+    M = sum(sizes)
+    exact, mag = _exact_on_device(*ops, dgrad)
+    for hint in (0, 1, max(sizes)):
+        out = torch.full((M + 5, P), 7.0, dtype=torch.bfloat16, device="cuda")
+        (mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(*ops, max_m_per_e=hint, out=out)
+        assert (out[M:] == 7.0).all()
+        err = (out[:M].double() - exact[:M]).abs()
+        assert (err <= BF16 * exact[:M].abs() + SUM_TOL * mag[:M]).all(), hint
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("sizes", [[150, 0, 133, 6], [3000, 0, 1100]])
+def test_tiled_product_of_small_integers_is_the_exact_sum_rounded(sizes, dgrad):
+    _say("tiled integers", sizes, dgrad)
+    P, R = 8208, 656
+    g = torch.Generator("cuda").manual_seed(8)
+    d = dict(device="cuda", generator=g)
+    codes = torch.from_numpy(ref.encode(np.arange(-3, 4))).cuda()
+    N, K = (R, P) if dgrad else (P, R)
+    M, E = sum(sizes), len(sizes)
+    q, w8 = codes[torch.randint(0, 7, (M, R), **d)], codes[torch.randint(0, 7, (E, N, K), **d)]
+    s = torch.exp2(torch.randint(0, 4, (-(-R // 128), M), **d).float())
+    ws = torch.exp2(torch.randint(-2, 2, (E, -(-N // 128), -(-K // 128)), **d).float())
+    off = torch.from_numpy(_offsets(sizes)).cuda()
+    exact, _ = _exact_on_device(q, s, w8, ws, off, dgrad)
+    # |sum| <= 656 * 9 * 8 * 2 < 2^17 in steps of 2^-2: exact in fp32 in any order
+    assert torch.equal((mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(q, s, w8, ws, off), exact.float().bfloat16())
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("sizes", [[140, 0, 129], [3000, 0, 1100]])
+def test_tiled_nan_stays_in_its_row(sizes, dgrad):
+    _say("tiled nan", sizes, dgrad)
+    q, s, w8, ws, off = _random_operands(sizes, 8208, 272, dgrad, 13)
+    q[1, 5] = 0x7F
+    s[1, 2] = np.inf
+    # behind the last row of a tile and of an expert
+    q[128, 0] = 0xFF
+    bad = torch.zeros(sum(sizes), dtype=torch.bool, device="cuda")
+    bad[[1, 2, 128]] = True
+    got = (mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(q, s, w8, ws, off)
+    assert torch.isnan(got[1]).all() and not torch.isfinite(got[2]).any() and torch.isnan(got[128]).all()
+    assert torch.isfinite(got[~bad]).all()
+
+
+def test_tiled_products_on_two_streams_and_in_a_graph():
+    _say("tiled graph")
+    dev = [(d, _random_operands(n, 8208, 400, d, 30)) for d in (False, True) for n in ([130, 0, 61], [3000, 0, 1100])]
+    run = lambda d, a, out=None: (mg.dgrad_fp8 if d else mg.fwd_fp8)(*a, out=out)   # noqa: E731
+    want = [run(d, a) for d, a in dev]
+    torch.cuda.synchronize()
+    got = []
+    for st in [torch.cuda.Stream() for _ in range(2)]:
+        with torch.cuda.stream(st):
+            got.append([run(d, a) for _ in range(2) for d, a in dev])
+    torch.cuda.synchronize()
+    for y in got:
+        assert all(torch.equal(v, want[i % len(dev)]) for i, v in enumerate(y))
+    outs = [torch.zeros_like(w) for w in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for (d, a), o in zip(dev, outs):
+            run(d, a, o)
+    for i in range(3):
+        for o in outs:
+            o.zero_()
+        for _, a in dev:
+            a[0].copy_(a[0].roll(1, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        for (d, a), o in zip(dev, outs):
+            assert torch.equal(o, run(d, a)), i
+
+
 # -- quantizers ------------------------------------------------------------------
 
 def _rows_input(M, K, dtype, seed):
