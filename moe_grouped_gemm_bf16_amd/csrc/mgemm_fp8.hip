@@ -846,15 +846,22 @@ int launch_fp8(bool dgrad, const Fp8Args& a, int64_t max_m, hipStream_t s) {
     // reads the rows half as often (16 rows, N = 4096: 17 against 20)
     return t64 <= cus ? few(fp8_few_rows_kernel<false, 2, 8, 2>, 32, 8, 4)
                       : few(fp8_few_rows_kernel<false, 4, 4, 2>, 64, 4, 8);
-  // Tiled: rounds of tiles over the chip times a round's time, in units of a
-  // 128 x 128 stage with one workgroup per compute unit.  A full round of
-  // stages measured 1.9 us (256 x 256), 1.15 us (128 x 128, two workgroups per
-  // compute unit) and 0.75 us (one): at K = N = M = 8192 the large tile is 20%
-  // faster, with fewer tiles than compute units the small one up to 30%.
+  // Tiled: the rounds of tiles over the chip times what a stage of a round
+  // takes: 2 us for 256 x 256 tiles, 1.25 us for 128 x 128 tiles with two
+  // workgroups per compute unit (0.9 us with one), less for a last round with
+  // so few tiles that they are halved.  Measured over 96 shapes, this picks the
+  // faster or one within 10% (us, large / small: FWD 8 experts, 2048 rows each,
+  // N = 4096, K = 2048: 154 / 166; 1024 rows: 88 / 85; 128 rows: 25 / 23; DGRAD
+  // 8 experts, 1024 rows, N = 4096, K = 2048: 108 / 96).
   auto tiles = [&](int64_t b) { return (2 * a.M / b + live + 1) / 2 * ((pdim + b - 1) / b); };
-  const double tb = (double)tiles(256) / cus, ts = (double)tiles(128) / cus;
-  const double big = 1.9 * (tb <= 0.5 ? 0.6 : tb <= 1.0 ? 1.0 : tb + 0.3);
-  const double small = ts <= 1.0 ? 0.75 : 1.15 * (ts <= 2.0 ? 1.0 : ts / 2 + 0.25);
+  auto rounds = [](double r, double full, double few, double last) {
+    const int64_t n = (int64_t)r;
+    const double part = r - (double)n;
+    return full * (double)n + (part == 0 ? 0 : part <= few ? last : full);
+  };
+  const int64_t ts = tiles(128);
+  const double big = rounds((double)tiles(256) / cus, 2.0, 0.5, 1.5);
+  const double small = ts <= cus ? 0.9 : rounds((double)ts / (2 * cus), 1.25, ts < 2 * cus ? 0 : 0.3, 0.4);
   if (big <= small)
     launch_tiled<Big>(dgrad, a, tile_bound(a, pdim, max_m, Big::BP, Big::BQ), cus, s);
   else

@@ -211,10 +211,11 @@ def test_two_streams_and_a_replayed_graph_give_the_eager_bits():
 
 # -- the tiled forms: enough 64-column pieces that the few-row form is not taken -----
 
-# rows per expert, output width, reduction; from 4000 rows on in the large tiles
+# rows per expert, output width, reduction; in the large tiles the last three
 TILED = [
     ([300], 8208, 144), ([127, 128, 129, 0, 1], 8208, 400), ([257, 40], 8400, 1536), ([33, 64, 2, 0, 0, 95], 8208, 720),
     ([200, 0, 184, 128], 8192, 16), ([4097], 8208, 144), ([2100, 0, 1877, 3], 8208, 272), ([1500, 0, 3000, 70, 1], 8336, 1040),
+    ([3400], 8208, 144), ([1700, 0, 1620, 3], 8208, 272),
 ]
 
 
