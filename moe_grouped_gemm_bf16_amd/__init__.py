@@ -759,6 +759,9 @@ def moe_route(logits: torch.Tensor, k: int, normalize: bool = True,
     weights, lse, prob_sum, loss = f.split_with_sizes((n, T, E, 2))
     experts, gather, token_rows, counts, tokens, offsets, work = i.split_with_sizes(
         (n, n, n, E, 1, local + 1, words))
+    # what a sum over ranks replaces has a version of its own: autograd's check
+    # of the saved others does not see it
+    counts, tokens, prob_sum = counts.data, tokens.data, prob_sum.data
     r = Route(weights.view(T, k), experts.view(T, k), lse, counts, prob_sum, tokens, loss, offsets,
               gather, token_rows.view(T, k))
     with _on(dev):

@@ -273,6 +273,13 @@ def test_route_replayed_graph_and_streams():
                 assert all(torch.equal(o[n], b) for o in outs)
 
 
+def test_sums_over_ranks_in_place_leave_the_saved_outputs_valid():
+    r = mg.moe_route(_logits(40, 16, torch.float32, 3).cuda(), 2)
+    for t in (r.counts, r.tokens, r.prob_sum):
+        t.add_(1)
+    assert all(t._version == 0 for t in (r.weights, r.experts, r.lse, r.loss, r.offsets, r.gather, r.token_rows))
+
+
 def test_bindings_refuse():
     l = torch.zeros(6, 8, device="cuda")
     with pytest.raises(ValueError, match="k must be"):
