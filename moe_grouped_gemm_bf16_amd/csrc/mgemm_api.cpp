@@ -279,7 +279,9 @@ mg_status fp8_product(bool dgrad, const void* q8, const float* qs, const void* w
   if (st != MG_OK) return st;
   if (max_m_per_e < 0 || (N & 15) || (K & 15)) return MG_ERR_SHAPE;
   const int64_t pdim = dgrad ? K : N, red = dgrad ? N : K;
-  // tile counts of the smallest tile (32 x 32) fit int32
+  // tile counts of the smallest tile (32 x 32) and the row behind the largest
+  // (256) fit int32
+  if (M > kMaxRows - 256) return MG_ERR_SHAPE;
   if (((M + 31) / 32 + E) * ((pdim + 31) / 32) > kMaxRows) return MG_ERR_SHAPE;
   if (M == 0 || pdim == 0) return MG_OK;
   if (!offsets || !out || (red > 0 && (!q8 || !qs || !w8 || !ws))) return MG_ERR_NULL;

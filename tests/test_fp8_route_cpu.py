@@ -144,6 +144,10 @@ def test_sizes_past_the_grid():
     assert h(A, 0, A, A, 1 << 24, 1, 16, None) == SHAPE
     assert h(A, 0, A, A, 1 << 12, 1 << 12, 1 << 14, None) == SHAPE
     assert h(None, 0, A, A, (1 << 24) - 1, 1, 16, None) == NUL            # the sizes alone are fine
+    # (x8, x_scale, w8, w_scale, offsets, y, M, N, K, E, max_m_per_e, stream)
+    for f in (L.mgemm_fwd_fp8, L.mgemm_dgrad_fp8):
+        assert f(A, A, A, A, A, A, 2 ** 31 - 256, 16, 16, 2, 0, None) == SHAPE      # the last tile's end
+        assert f(A, A, A, A, None, A, 2 ** 31 - 257, 16, 16, 2, 0, None) == NUL     # the sizes alone are fine
     # T k past 64 bits
     assert L.mg_moe_route(*_route_args(T=1 << 58, E=64, k=64, local=64)) == SHAPE
     assert L.mg_moe_route_workspace(2 ** 63 - 1, 64) == 0
