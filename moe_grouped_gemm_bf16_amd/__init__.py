@@ -10,6 +10,10 @@ kernels; PyTorch provides device memory and the current stream.
   fwd_swiglu(x, w13, offsets, gather)                  gate-up forward, SwiGLU fused,
       h[i] = silu(x[r] w1[e]^T) * (x[r] w3[e]^T), r = gather[i]   rows gathered by index
   grouped_list([(A_g, B_g), ...])   D_g = A_g B_g^T    independent GEMMs, per-group shapes
+  moe_route(logits, k)    gate, row order, balance and z losses; moe_route_bwd, its gradient
+  moe_combine(rows, token_rows, weights)               and moe_combine_bwd, its gradient
+  fwd_fp8, dgrad_fp8      block-scaled fp8 products on the codes of fp8_quantize,
+      fp8_quantize_swiglu and fp8_quantize_weights
 
 Page-shaped aliases follow the RapidGEMM README ("Kernels"):
   Mgemm(x, w, cnt, max_M_per_E, transpose_B) and Kgemm(grad, X, cnt, descriptor).
@@ -30,33 +34,22 @@ __all__ = ["fwd", "dgrad", "wgrad", "wgrad_noalloc", "fwd_swiglu", "dgrad_swiglu
            "MgemmError", "status_str", "LIB"]
 
 
-# The current stream's handle without building a torch.cuda.Stream object (2 us
-# of a call's 12), where this torch has that call.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and the current stream's handle, without the Python objects
+# that the public calls make (2 us of a call), where this torch has these calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream(t: torch.Tensor) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(t.device.index)
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-class _Here:
-    """The device context of tensors that are on the current device."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _on(dev: torch.device):
-    """torch.cuda.device(dev), or nothing where dev is current already."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _run(name: str, dev: torch.device, *args) -> None:
+    """LIB.name(*args, stream) with dev current, on its current stream."""
+    index = dev.index
+    if index == _current_device():
+        status = getattr(LIB, name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(LIB, name)(*args, _raw_stream(index))
+    check(status, name)
 
 
 def _ptr(t: torch.Tensor | None) -> int:
@@ -111,10 +104,8 @@ def fwd(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, max_m_per_e: in
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
     _same_device(x.device, w=w, out=out)
-    with _on(x.device):
-        st = LIB.mgemm_fwd(x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                           M, N, K, E, int(max_m_per_e), _stream(x))
-    check(st, "mgemm_fwd")
+    _run("mgemm_fwd", x.device, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), M,
+         N, K, E, int(max_m_per_e))
     return out
 
 
@@ -137,10 +128,8 @@ def dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, max_m_per_e:
         if tuple(out.shape) != (M, K):
             raise ValueError(f"out must be [{M}, {K}]")
     _same_device(dy.device, w=w, out=out)
-    with _on(dy.device):
-        st = LIB.mgemm_dgrad(dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                             M, N, K, E, int(max_m_per_e), _stream(dy))
-    check(st, "mgemm_dgrad")
+    _run("mgemm_dgrad", dy.device, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
+         M, N, K, E, int(max_m_per_e))
     return out
 
 
@@ -183,10 +172,8 @@ def _wgrad(fn: str, dy, x, offsets, E, out, accumulate):
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dy.device, x=x, out=out)
-    with _on(dy.device):
-        st = getattr(LIB, fn)(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                              M, N, K, E, 1 if accumulate else 0, _stream(dy))
-    check(st, fn)
+    _run(fn, dy.device, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(), M, N, K, E,
+         1 if accumulate else 0)
     return out
 
 
@@ -235,11 +222,8 @@ def fwd_swiglu(x: torch.Tensor, w13: torch.Tensor, offsets: torch.Tensor,
             raise ValueError(f"gu_out must be [{M}, {2 * I}]")
         guptr = gu_out.data_ptr()
     _same_device(x.device, w13=w13, out=out, gu_out=gu_out)
-    with _on(x.device):
-        st = LIB.mgemm_fwd_swiglu_gu(x.data_ptr(), gptr, w13.data_ptr(), offsets.data_ptr(),
-                                     out.data_ptr(), guptr, M, T, I, K, E, int(max_m_per_e),
-                                     _stream(x))
-    check(st, "mgemm_fwd_swiglu_gu")
+    _run("mgemm_fwd_swiglu_gu", x.device, x.data_ptr(), gptr, w13.data_ptr(), offsets.data_ptr(),
+         out.data_ptr(), guptr, M, T, I, K, E, int(max_m_per_e))
     return out
 
 
@@ -267,11 +251,8 @@ def dgrad_swiglu(dy: torch.Tensor, w2: torch.Tensor, gu: torch.Tensor, offsets: 
         if tuple(out.shape) != (M, 2 * I):
             raise ValueError(f"out must be [{M}, {2 * I}]")
     _same_device(dy.device, w2=w2, gu=gu, out=out)
-    with _on(dy.device):
-        st = LIB.mgemm_dgrad_swiglu(dy.data_ptr(), w2.data_ptr(), gu.data_ptr(),
-                                    offsets.data_ptr(), out.data_ptr(), M, N, I, E,
-                                    int(max_m_per_e), _stream(dy))
-    check(st, "mgemm_dgrad_swiglu")
+    _run("mgemm_dgrad_swiglu", dy.device, dy.data_ptr(), w2.data_ptr(), gu.data_ptr(),
+         offsets.data_ptr(), out.data_ptr(), M, N, I, E, int(max_m_per_e))
     return out
 
 
@@ -314,9 +295,7 @@ def grouped_list_desc(desc: torch.Tensor, G: int) -> None:
     """mgemm_list on a device descriptor array (from list_descriptors)."""
     if desc.dtype != torch.uint8 or not desc.is_cuda or desc.numel() != 48 * G:
         raise ValueError("desc must be the device uint8 array of G descriptors")
-    with _on(desc.device):
-        st = LIB.mgemm_list(desc.data_ptr(), int(G), _stream(desc))
-    check(st, "mgemm_list")
+    _run("mgemm_list", desc.device, desc.data_ptr(), int(G))
 
 
 def grouped_list(groups, outs=None):
@@ -352,10 +331,8 @@ def mx_scales_blocked(scales: torch.Tensor, out: torch.Tensor | None = None) -> 
         if tuple(out.shape) != shape:
             raise ValueError(f"out must be {shape}")
     _same_device(scales.device, out=out)
-    with _on(scales.device):
-        st = LIB.mg_mx_scales_blocked(scales.data_ptr(), out.data_ptr(), rows, 32 * nb, batch,
-                                      _stream(scales))
-    check(st, "mg_mx_scales_blocked")
+    _run("mg_mx_scales_blocked", scales.device, scales.data_ptr(), out.data_ptr(), rows, 32 * nb,
+         batch)
     return out
 
 
@@ -387,28 +364,28 @@ def fwd_mx(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scale: t
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
     _same_device(x8.device, x_scale=x_scale, w8=w8, w_scale=w_scale, out=out)
-    with _on(x8.device):
-        st = LIB.mgemm_fwd_mx(x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
-                              offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e),
-                              _stream(x8))
-    check(st, "mgemm_fwd_mx")
+    _run("mgemm_fwd_mx", x8.device, x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(),
+         w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e))
     return out
 
 
-def _codes_out(M, K, dev, out, scales, shape):
+def _codes_out(M, K, dev, out, scales):
+    # (sizes as separate arguments: 1.3 us of the host's time, as a tuple 1.6)
     nb = (K + 127) // 128
     if out is None:
-        out = torch.empty(shape + (K,), dtype=torch.uint8, device=dev)
+        out = torch.empty(M, K, dtype=torch.uint8, device=dev)
     else:
-        _need(out, "out", torch.uint8, len(shape) + 1)
-        if tuple(out.shape) != shape + (K,):
-            raise ValueError(f"out must be {list(shape + (K,))}")
+        _need(out, "out", torch.uint8, 2)
+        if tuple(out.shape) != (M, K):
+            raise ValueError(f"out must be {[M, K]}")
+        _same_device(dev, out=out)
     if scales is None:
-        scales = torch.empty((nb, M), dtype=torch.float32, device=dev)
+        scales = torch.empty(nb, M, dtype=torch.float32, device=dev)
     else:
         _need(scales, "scales", torch.float32, 2)
         if tuple(scales.shape) != (nb, M):
             raise ValueError(f"scales must be [{nb}, {M}]")
+        _same_device(dev, scales=scales)
     return out, scales
 
 
@@ -441,13 +418,9 @@ def fp8_quantize(x: torch.Tensor, gather: torch.Tensor | None = None,
         _same_device(x.device, gather=gather)
         M = gather.numel()
     E = _rows_offsets(offsets, x.device)
-    out, scales = _codes_out(M, K, x.device, out, scales, (M,))
-    _same_device(x.device, out=out, scales=scales)
-    with _on(x.device):
-        st = LIB.mg_fp8_quantize(x.data_ptr(), 1 if x.dtype == torch.float32 else 0, _ptr(gather),
-                                 _ptr(offsets), out.data_ptr(), scales.data_ptr(), M, T, K, E,
-                                 _stream(x))
-    check(st, "mg_fp8_quantize")
+    out, scales = _codes_out(M, K, x.device, out, scales)
+    _run("mg_fp8_quantize", x.device, x.data_ptr(), 1 if x.dtype == torch.float32 else 0,
+         _ptr(gather), _ptr(offsets), out.data_ptr(), scales.data_ptr(), M, T, K, E)
     return out, scales
 
 
@@ -460,12 +433,9 @@ def fp8_quantize_swiglu(gu: torch.Tensor, offsets: torch.Tensor | None = None,
     if I2 % 2:
         raise ValueError(f"gu must hold two halves (2I columns), got {I2}")
     E = _rows_offsets(offsets, gu.device)
-    out, scales = _codes_out(M, I2 // 2, gu.device, out, scales, (M,))
-    _same_device(gu.device, out=out, scales=scales)
-    with _on(gu.device):
-        st = LIB.mg_fp8_quantize_swiglu(gu.data_ptr(), _ptr(offsets), out.data_ptr(),
-                                        scales.data_ptr(), M, I2 // 2, E, _stream(gu))
-    check(st, "mg_fp8_quantize_swiglu")
+    out, scales = _codes_out(M, I2 // 2, gu.device, out, scales)
+    _run("mg_fp8_quantize_swiglu", gu.device, gu.data_ptr(), _ptr(offsets), out.data_ptr(),
+         scales.data_ptr(), M, I2 // 2, E)
     return out, scales
 
 
@@ -480,22 +450,20 @@ def fp8_quantize_weights(w: torch.Tensor, out: torch.Tensor | None = None,
     E, N, K = w.shape
     shape = (E, (N + 127) // 128, (K + 127) // 128)
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
+        out = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
     else:
         _need(out, "out", torch.uint8, 3)
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=w.device)
+        scales = torch.empty(*shape, dtype=torch.float32, device=w.device)
     else:
         _need(scales, "scales", torch.float32, 3)
         if tuple(scales.shape) != shape:
             raise ValueError(f"scales must be {list(shape)}")
     _same_device(w.device, out=out, scales=scales)
-    with _on(w.device):
-        st = LIB.mg_fp8_quantize_weights(w.data_ptr(), 1 if w.dtype == torch.float32 else 0,
-                                         out.data_ptr(), scales.data_ptr(), E, N, K, _stream(w))
-    check(st, "mg_fp8_quantize_weights")
+    _run("mg_fp8_quantize_weights", w.device, w.data_ptr(), 1 if w.dtype == torch.float32 else 0,
+         out.data_ptr(), scales.data_ptr(), E, N, K)
     return out, scales
 
 
@@ -539,17 +507,14 @@ def _product_fp8(fn, dgrad, q8, q_scale, w8, w_scale, offsets, max_m_per_e, out)
     _offsets(offsets, E, q8.device)
     P = K if dgrad else N
     if out is None:
-        out = torch.empty((M, P), dtype=torch.bfloat16, device=q8.device)
+        out = torch.empty(M, P, dtype=torch.bfloat16, device=q8.device)
     else:
         _need(out, "out", torch.bfloat16, 2)
         if tuple(out.shape) != (M, P):
             raise ValueError(f"out must be [{M}, {P}]")
-    _same_device(q8.device, w8=w8, out=out, **{scale: q_scale, "w_scale": w_scale})
-    with _on(q8.device):
-        st = getattr(LIB, fn)(q8.data_ptr(), q_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
-                              offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e),
-                              _stream(q8))
-    check(st, fn)
+    _same_device(q8.device, w8=w8, out=out, w_scale=w_scale, **{scale: q_scale})
+    _run(fn, q8.device, q8.data_ptr(), q_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
+         offsets.data_ptr(), out.data_ptr(), M, N, K, E, int(max_m_per_e))
     return out
 
 
@@ -584,11 +549,9 @@ def wgrad_mx(dyt8: torch.Tensor, dyt_scale: torch.Tensor, xt8: torch.Tensor,
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dyt8.device, dyt_scale=dyt_scale, xt8=xt8, xt_scale=xt_scale, out=out)
-    with _on(dyt8.device):
-        st = LIB.kgemm_wgrad_mx(dyt8.data_ptr(), dyt_scale.data_ptr(), xt8.data_ptr(),
-                                xt_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                                M, N, K, E, 1 if accumulate else 0, _stream(dyt8))
-    check(st, "kgemm_wgrad_mx")
+    _run("kgemm_wgrad_mx", dyt8.device, dyt8.data_ptr(), dyt_scale.data_ptr(), xt8.data_ptr(),
+         xt_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), M, N, K, E,
+         1 if accumulate else 0)
     return out
 
 
@@ -625,11 +588,8 @@ def wgrad_mx_tm(dy8: torch.Tensor, dy_scale: torch.Tensor, x8: torch.Tensor,
         if tuple(out.shape) != (E, N, K):
             raise ValueError(f"out must be [{E}, {N}, {K}]")
     _same_device(dy8.device, dy_scale=dy_scale, x8=x8, x_scale=x_scale, out=out)
-    with _on(dy8.device):
-        st = LIB.kgemm_wgrad_mx_tm(dy8.data_ptr(), dy_scale.data_ptr(), x8.data_ptr(),
-                                   x_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                                   M, N, K, E, 1 if accumulate else 0, _stream(dy8))
-    check(st, "kgemm_wgrad_mx_tm")
+    _run("kgemm_wgrad_mx_tm", dy8.device, dy8.data_ptr(), dy_scale.data_ptr(), x8.data_ptr(),
+         x_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), M, N, K, E, 1 if accumulate else 0)
     return out
 
 
@@ -658,10 +618,8 @@ def moe_combine(rows: torch.Tensor, token_rows: torch.Tensor,
         if tuple(out.shape) != (T, D):
             raise ValueError(f"out must be [{T}, {D}]")
     _same_device(rows.device, token_rows=token_rows, weights=weights, out=out)
-    with _on(rows.device):
-        st = LIB.mg_moe_combine(rows.data_ptr(), token_rows.data_ptr(), wptr, out.data_ptr(),
-                                M, T, k, D, _stream(rows))
-    check(st, "mg_moe_combine")
+    _run("mg_moe_combine", rows.device, rows.data_ptr(), token_rows.data_ptr(), wptr,
+         out.data_ptr(), M, T, k, D)
     return out
 
 
@@ -685,7 +643,7 @@ def moe_combine_bwd(dout: torch.Tensor, rows: torch.Tensor, token_rows: torch.Te
         _need(weights, "weights", torch.float32, 2)
         if tuple(weights.shape) != (T, k):
             raise ValueError(f"weights must be [{T}, {k}]")
-        dweights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+        dweights = torch.empty(T, k, dtype=torch.float32, device=rows.device)
     if drows is None:
         drows = torch.zeros((M, D), dtype=torch.bfloat16, device=rows.device)
     else:
@@ -693,11 +651,8 @@ def moe_combine_bwd(dout: torch.Tensor, rows: torch.Tensor, token_rows: torch.Te
         if tuple(drows.shape) != (M, D):
             raise ValueError(f"drows must be [{M}, {D}]")
     _same_device(rows.device, dout=dout, token_rows=token_rows, weights=weights, drows=drows)
-    with _on(rows.device):
-        st = LIB.mg_moe_combine_bwd(dout.data_ptr(), rows.data_ptr(), token_rows.data_ptr(),
-                                    _ptr(weights), drows.data_ptr(), _ptr(dweights), M, T, k, D,
-                                    _stream(rows))
-    check(st, "mg_moe_combine_bwd")
+    _run("mg_moe_combine_bwd", rows.device, dout.data_ptr(), rows.data_ptr(), token_rows.data_ptr(),
+         _ptr(weights), drows.data_ptr(), _ptr(dweights), M, T, k, D)
     return drows, dweights
 
 
@@ -764,15 +719,11 @@ def moe_route(logits: torch.Tensor, k: int, normalize: bool = True,
     counts, tokens, prob_sum = counts.data, tokens.data, prob_sum.data
     r = Route(weights.view(T, k), experts.view(T, k), lse, counts, prob_sum, tokens, loss, offsets,
               gather, token_rows.view(T, k))
-    with _on(dev):
-        st = LIB.mg_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
-                              _ptr(mask), T, E, k, 1 if normalize else 0, int(first), local,
-                              r.weights.data_ptr(), r.experts.data_ptr(), r.lse.data_ptr(),
-                              r.counts.data_ptr(), r.prob_sum.data_ptr(), r.tokens.data_ptr(),
-                              r.loss.data_ptr(), r.offsets.data_ptr(), r.gather.data_ptr(),
-                              r.token_rows.data_ptr(), work.data_ptr(), 4 * words,
-                              _stream(logits))
-    check(st, "mg_moe_route")
+    _run("mg_moe_route", dev, logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
+         _ptr(mask), T, E, k, 1 if normalize else 0, int(first), local, r.weights.data_ptr(),
+         r.experts.data_ptr(), r.lse.data_ptr(), r.counts.data_ptr(), r.prob_sum.data_ptr(),
+         r.tokens.data_ptr(), r.loss.data_ptr(), r.offsets.data_ptr(), r.gather.data_ptr(),
+         r.token_rows.data_ptr(), work.data_ptr(), 4 * words)
     return r
 
 
@@ -814,12 +765,10 @@ def moe_route_bwd(logits: torch.Tensor, weights: torch.Tensor, experts: torch.Te
             raise ValueError(f"out must be [{T}, {E}]")
     _same_device(logits.device, weights=weights, experts=experts, lse=lse, counts=counts,
                  tokens=tokens, dweights=dweights, dloss=dloss, out=out)
-    with _on(logits.device):
-        st = LIB.mg_moe_route_bwd(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
-                                  weights.data_ptr(), experts.data_ptr(), lse.data_ptr(),
-                                  counts.data_ptr(), tokens.data_ptr(), _ptr(dweights), _ptr(dloss),
-                                  out.data_ptr(), T, E, k, 1 if normalize else 0, _stream(logits))
-    check(st, "mg_moe_route_bwd")
+    _run("mg_moe_route_bwd", logits.device, logits.data_ptr(),
+         1 if logits.dtype == torch.bfloat16 else 0, weights.data_ptr(), experts.data_ptr(),
+         lse.data_ptr(), counts.data_ptr(), tokens.data_ptr(), _ptr(dweights), _ptr(dloss),
+         out.data_ptr(), T, E, k, 1 if normalize else 0)
     return out
 
 
