@@ -383,9 +383,10 @@ mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, fl
  * the blocks by fp32 fmas in ascending order, or, for few rows per expert, in
  * four or eight such sums added in a fixed order: results are bitwise
  * reproducible.  M at most 2^31 - 257, N and K multiples of 16.  x8, w8, y
- * 16-byte aligned, scales 4-byte aligned.  Rows i >= offsets[E] of y are not touched.  M == 0 or N == 0 is a no-op;
- * K == 0 writes zeros.  Allocates nothing.  max_m_per_e: launch-size hint, as
- * for mgemm_fwd (results do not depend on it). */
+ * 16-byte aligned, scales 4-byte aligned.  Rows i >= offsets[E] of y are not
+ * touched.  M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Allocates
+ * nothing.  max_m_per_e: launch-size hint, as for mgemm_fwd (results do not
+ * depend on it). */
 mg_status mgemm_fwd_fp8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
                         const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int32_t E,
                         int64_t max_m_per_e, void* stream);
