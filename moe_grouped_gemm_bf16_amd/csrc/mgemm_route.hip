@@ -724,7 +724,7 @@ template <typename T, int L, int V>
 __global__ __launch_bounds__(kBT) void route_bwd_kernel(RouteBwdArgs a) {
   using LN = Lanes<T, L, V>;
   extern __shared__ __attribute__((aligned(16))) float gate[];       // [kBT / L][E]
-  __shared__ int csum[kBT / 64];
+  __shared__ long long csum[kBT / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = threadIdx.x % L;
   float* mine = gate + (threadIdx.x / L) * a.E;
   const bool losses = a.dloss != nullptr;
@@ -732,7 +732,7 @@ __global__ __launch_bounds__(kBT) void route_bwd_kernel(RouteBwdArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) g[v] = 0.f;
   if (losses) {
-    int c = 0;
+    long long c = 0;                     // (sums over ranks may pass 31 bits together)
     for (int e = threadIdx.x; e < a.E; e += kBT) c += a.counts[e];
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) c += __shfl_xor(c, d, 64);

@@ -188,6 +188,20 @@ def test_counts_summed_over_ranks_enter_the_gradient():
     assert (np.abs(_np(d) - exact) <= G_TOL * mag).all()
 
 
+def test_counts_over_ranks_that_pass_31_bits_together():
+    _say("large counts")
+    l = _logits(200, 16, torch.float32, 8)
+    r = mg.moe_route(l.cuda(), 2)
+    want = ref.route(l.double().numpy(), 2, True)
+    counts = torch.full((16,), 1 << 28, dtype=torch.int32)                  # 2^32 in all
+    counts[3] = (1 << 31) - 1
+    want["counts"], want["tokens"] = counts.numpy().astype(np.int64), np.array([(1 << 31) - 1], np.int64)
+    d = mg.moe_route_bwd(l.cuda(), r.weights, r.experts, r.lse, counts.cuda(), torch.full((1,), (1 << 31) - 1, dtype=torch.int32, device="cuda"),
+                         None, torch.tensor([1e9, 1e9]).cuda())
+    exact, mag = ref.route_bwd(want, None, np.array([1e9, 1e9]), True)
+    assert (np.abs(_np(d) - exact) <= G_TOL * mag).all()
+
+
 @pytest.mark.parametrize("T,k,D", [(1, 1, 8), (5, 8, 264), (100, 3, 2048), (33, 64, 520), (300, 2, 72)])
 def test_combine_gradient(T, k, D):
     _say("combine_bwd", T, k, D)
