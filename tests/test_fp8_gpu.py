@@ -413,6 +413,19 @@ def test_quantize_weights_bits(E, N, K, dtype):
         assert (_np(codes[e]) == want).all() and (_np(scales[e]) == ws).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,N,K", [(5, 300, 272), (9, 128, 1168), (17, 40, 128)])
+def test_quantize_weights_of_many_block_rows_bits(E, N, K, dtype):
+    # from eight rows of blocks on, their order over the workgroups differs
+    _say("quantize weights rows", E, N, K, dtype)
+    w = (torch.from_numpy(np.random.default_rng(E + N).standard_normal((E, N, K))) / 16).to(dtype)
+    w *= torch.exp2(torch.arange(E, dtype=torch.float32))[:, None, None].to(dtype)
+    codes, scales = mg.fp8_quantize_weights(w.cuda())
+    for e in range(E):
+        want, ws = ref.quantize(w[e].float().numpy(), 128)
+        assert (_np(codes[e]) == want).all() and (_np(scales[e]) == ws).all()
+
+
 def test_quantize_past_32_bit_offsets():
     M, K = 140001, 16400
     _say("quantize large", M, K)
