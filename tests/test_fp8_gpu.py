@@ -175,6 +175,53 @@ def test_products_past_32_bit_offsets():
         assert ((got - want).abs() <= (BF16 + SUM_TOL) * want.abs()).all()        # all terms positive
 
 
+def _sampled(q, s, w8, ws, dgrad, y, rows, cols):
+    """Outputs (rows, cols) of the last expert against exact sums, all terms positive."""
+    table = torch.from_numpy(ref.e4m3_values()).cuda()
+    R, K = q.shape[1], w8.shape[2]
+    x = table[q[rows].int()] * s[:, rows].t().double().repeat_interleave(128, 1)[:, :R]
+    blk = ws[-1].double()
+    if dgrad:
+        want = torch.stack([(x * (table[w8[-1][:, c].int()] * blk[:, c // 128].repeat_interleave(128)[:R])).sum(1) for c in cols.tolist()], 1)
+    else:
+        w = table[w8[-1][cols].int()] * blk[cols // 128].repeat_interleave(128, 1)[:, :K]
+        want = (x[:, None] * w[None]).sum(2)
+    # a block's sum 2^-11, the fmas over the blocks, the result's rounding
+    tol = BF16 + 2.0 ** -11 + (-(-R // 128) + 4) * 2.0 ** -24
+    assert ((y[rows][:, cols].double() - want).abs() <= tol * want.abs()).all()
+
+
+@pytest.mark.parametrize("M", [100, 700])
+def test_every_form_past_32_bit_offsets(M):
+    # 5.4 GB of weights; 100 rows take the few-row forms, 700 the tiled ones
+    E, N, K = 21, 16384, 15728
+    _say("large", E, N, K, M)
+    g = torch.Generator("cuda").manual_seed(M)
+    d = dict(device="cuda", generator=g)
+    w8 = torch.randint(0, 120, (E, N, K), dtype=torch.uint8, **d)
+    ws = torch.rand(E, N // 128, -(-K // 128), **d) * 1e-4
+    off = torch.tensor([0] * E + [M], dtype=torch.int32, device="cuda")
+    for dgrad in (False, True):
+        R = N if dgrad else K
+        q, s = torch.randint(0, 120, (M, R), dtype=torch.uint8, **d), torch.rand(-(-R // 128), M, **d) * 1e-4
+        y = (mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(q, s, w8, ws, off)
+        _sampled(q, s, w8, ws, dgrad, y, torch.tensor([0, 31, 64, M - 1], device="cuda"), torch.tensor([0, 1, 5000, (K if dgrad else N) - 1], device="cuda"))
+
+
+@pytest.mark.parametrize("M,P,R", [(3, 128, 2 ** 22), (70, 64, 2 ** 22), (300, 8208, 2 ** 18)])
+def test_long_reductions(M, P, R):
+    _say("long", M, P, R)
+    g = torch.Generator("cuda").manual_seed(R)
+    d = dict(device="cuda", generator=g)
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    for dgrad in (False, True):
+        N, K = (R, P) if dgrad else (P, R)
+        w8, ws = torch.randint(0, 100, (1, N, K), dtype=torch.uint8, **d), torch.rand(1, -(-N // 128), -(-K // 128), **d) * 1e-4
+        q, s = torch.randint(0, 100, (M, R), dtype=torch.uint8, **d), torch.rand(-(-R // 128), M, **d) * 1e-4
+        y = (mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(q, s, w8, ws, off)
+        _sampled(q, s, w8, ws, dgrad, y, torch.tensor([0, M - 1], device="cuda"), torch.tensor([0, 63, P - 1], device="cuda"))
+
+
 def test_two_streams_and_a_replayed_graph_give_the_eager_bits():
     _say("streams and graph")
     cases = [(False, *_operands([130, 0, 61], 272, 400, False, 21)), (False, *_operands([2, 0, 1], 272, 400, False, 22)),
