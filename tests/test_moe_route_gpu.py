@@ -61,6 +61,18 @@ def test_route(i, dtype):
     _check_route(mg.moe_route(l.cuda(), k, normalize=i % 2 == 0), l, k, i % 2 == 0)
 
 
+@pytest.mark.parametrize("T,E,k", [(256, 100, 64), (40000, 80, 40), (600000, 8, 4)])
+def test_route_of_many_entries_per_workgroup(T, E, k):
+    # more entries than a wave holds in registers between counting and placing.
+    # prob_sum: at most 37 + 38 additions in a row, 2^-17.8, beside a
+    # probability's 2^-18.5 (|l - max| < 20): within 2^-17
+    _say("route entries", T, E, k)
+    l = _logits(T, E, torch.float32, T)
+    _check_route(mg.moe_route(l.cuda(), k), l, k, True)
+    m = torch.rand(T, generator=torch.Generator().manual_seed(1)) < 0.9
+    _check_route(mg.moe_route(l.cuda(), k, normalize=False, mask=m.cuda(), first=1, local=E - 3), l, k, False, m, 1, E - 3)
+
+
 @pytest.mark.parametrize("T", [5, 700])
 def test_route_mask_infinities_nan_and_lowest_values(T):
     _say("route masks", T)
