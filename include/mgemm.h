@@ -376,8 +376,10 @@ mg_status mg_fp8_quantize_weights(const void* w, int32_t w_fp32, void* codes, fl
  * x8: uint8 E4M3 codes [M, K]; x_scale: fp32 [ceil(K/128), M]; w8: uint8
  * [E, N, K]; w_scale: fp32 [E, ceil(N/128), ceil(K/128)]; y: bf16 [M, N]
  * (written, round to nearest even).  mg_fp8_quantize and
- * mg_fp8_quantize_weights make these operands.  A scale may be any fp32 value;
- * a NaN code or scale makes NaN in the outputs that it enters and no others.
+ * mg_fp8_quantize_weights make these operands.  A scale may be any fp32 value,
+ * also where the product of a row's and a block's is none (below 2^-150 it
+ * counts as zero); a NaN code or scale makes NaN in the outputs that it enters
+ * and no others.
  * Each block's 128 products are summed by the fp8 matrix-core instruction
  * (measured exact to 1.5e-5 of a block's sum for normally distributed values),
  * the blocks by fp32 fmas in ascending order, or, for few rows per expert, in

@@ -116,6 +116,24 @@ __device__ __forceinline__ f32x4 product(const i32x8& p, const i32x8& q) {
                                                           127, 0, 127);
 }
 
+// The factor of a block's sum is its two scales' product s.  Where that is odd,
+// neither a normal number nor zero, it is taken as m c, c = 2^+-64: a sum (0, or
+// 2^-18 to 2^24.6) times c is exact, and that times m is rounded once, as with a
+// factor that fits.  (Zero from an underflow drops a block that adds less than
+// 2^-125, 2^-150 times 128 products of at most 448^2.  m past the largest number
+// is that, so that a sum of zero stays zero; an infinite or NaN scale stays so.)
+struct Factor {
+  float m, c;
+};
+__device__ __forceinline__ bool factor_odd(float s) { return __builtin_amdgcn_classf(s, 0x297); }
+__device__ __forceinline__ Factor split_factor(float a, float b, float s) {
+  const bool small = fabsf(s) < 1.0f;
+  const float k = small ? 0x1p32f : 0x1p-32f;
+  float m = (a * k) * (b * k);
+  if (fabsf(a) <= 3.40282347e38f && fabsf(b) <= 3.40282347e38f) m = fminf(fmaxf(m, -3.40282347e38f), 3.40282347e38f);
+  return {m, small ? 0x1p-64f : 0x1p64f};
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
@@ -557,8 +575,6 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
     }
     for (int kt = 0; kt < nk; ++kt) {
       float s[C::MQ];
-#pragma unroll
-      for (int j = 0; j < C::MQ; ++j) s[j] = rawq[j] * raww;
       f32x4 part[2][C::MQ];
       // result block (i, j) of the stage into its accumulator.  The empty use
       // pins it here: a product has no side effects, and the compiler would
@@ -588,6 +604,39 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
           if (last) fq[j] = readQ(lds + cbuf, j);
           if (i > 0) add(i - 1, j);
         }
+        if (i == 0) {                                // (under the first products, no sums to add yet)
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < C::MQ; ++j) {
+            asm volatile("" ::"v"(part[0][j]));      // (not moved behind the branch)
+            s[j] = rawq[j] * raww;
+            odd |= factor_odd(s[j]);
+          }
+          if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd) != 0, 0)) {
+            // rows with an odd factor: the stage is added to them here, and with
+            // the factor 0 below (the check costs at most 1% where tiles are
+            // small: 8 experts, 512 rows each, N = 768, K = 2512: 24.9 -> 25.2 us)
+            Factor f[C::MQ];
+#pragma unroll
+            for (int j = 0; j < C::MQ; ++j) {
+              f[j] = factor_odd(s[j]) ? split_factor(rawq[j], raww, s[j]) : Factor{0.f, 1.f};
+              if (factor_odd(s[j])) s[j] = 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < C::MP; ++r) {
+              const i32x8 p = readP(st, r);
+#pragma unroll
+              for (int j = 0; j < C::MQ; ++j) {
+                const f32x4 v = product(p, fq[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  acc[r][j][e] = __builtin_fmaf(v[e] * f[j].c, f[j].m, acc[r][j][e]);
+                // (one at a time: with more registers here the usual path is 2% slower)
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -614,7 +663,7 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
 constexpr int kFewQ = 32;
 
 template <bool DG, int PB, int NW, int U>
-__global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8Args a) {
+__global__ __launch_bounds__(64 * NW, DG || PB == 2 ? 4 : 3) void fp8_few_rows_kernel(Fp8Args a) {
   constexpr int P = 16 * PB;
   static_assert(128 % P == 0, "one weight scale per tile and block");
   static_assert(!DG || PB == 4, "the weights' places in LDS");
@@ -728,20 +777,23 @@ __global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8Args a) {
 #pragma unroll
           for (int i = 0; i < PB; ++i) fw[u][i] = staged(u, i);
         }
-#pragma unroll
-        for (int i = 0; i < PB; ++i) {
-          const f32x4 p = product(fw[u][i], fx[u][0]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][0][e] = __builtin_fmaf(p[e], s[u][0], acc[i][0][e]);
-        }
-        if (two) {
+        auto add = [&](int h) {
+          Factor f = {s[u][h], 1.f};
+          if (__builtin_expect(__builtin_amdgcn_ballot_w64(factor_odd(f.m)) != 0, 0)) {
+            // from the two scales, read again (a factor of a block past nk or of
+            // a row past the last is zero, so the address is in the scales)
+            const int kb = min(k0 + NW * u, nk - 1);
+            if (factor_odd(f.m)) f = split_factor(a.qs[(int64_t)kb * a.M + t.q0 + 16 * h + l16], wsc[kb * sblock], f.m);
+          }
 #pragma unroll
           for (int i = 0; i < PB; ++i) {
-            const f32x4 p = product(fw[u][i], fx[u][1]);
+            const f32x4 p = product(fw[u][i], fx[u][h]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][1][e] = __builtin_fmaf(p[e], s[u][1], acc[i][1][e]);
+            for (int e = 0; e < 4; ++e) acc[i][h][e] = __builtin_fmaf(p[e] * f.c, f.m, acc[i][h][e]);
           }
-        }
+        };
+        add(0);
+        if (two) add(1);
       }
     }
     auto sums = [&](int v) { return reinterpret_cast<f32x4*>(own[v]); };
