@@ -814,7 +814,9 @@ __global__ __launch_bounds__(kBT) void route_bwd_kernel(RouteBwdArgs a) {
       __builtin_amdgcn_wave_barrier();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    const float common = zc * lse - pg - (a.normalize ? 0.f : dot);
+    // (the z term as (p lse) zc: lse is up to the largest number, zc may be above
+    // one, and p is what keeps their product one)
+    const float common = -pg - (a.normalize ? 0.f : dot);
     T* out = static_cast<T*>(a.dlogits) + tt * a.E;
 #pragma unroll
     for (int b = 0; b < V / LN::C; ++b) {
@@ -823,7 +825,7 @@ __global__ __launch_bounds__(kBT) void route_bwd_kernel(RouteBwdArgs a) {
 #pragma unroll
       for (int c = 0; c < LN::C; ++c) {
         const int v = b * LN::C + c;
-        float d = p[v] * (g[v] + common);
+        float d = __builtin_fmaf(p[v] * lse, zc, p[v] * (g[v] + common));
         if (a.dweights != nullptr && e0 + c < a.E) d += mine[e0 + c];
         if constexpr (sizeof(T) == 4) tmp[c] = d;
         else tmp[c] = __builtin_bit_cast(uint16_t, (__bf16)d);
