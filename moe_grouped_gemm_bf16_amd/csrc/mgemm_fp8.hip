@@ -140,9 +140,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // ---------------------------------------------------------------- scheduler --
 
-// The experts' row ranges and tile counts, in LDS: offs[e] is the clamped,
-// non-decreasing offset (a broken offsets array then cannot move an access out
-// of the tensors), pref[e] the exclusive prefix of ceil(rows / BQ).
+// The experts' row ranges and tile counts, in LDS: offs[e] is the running
+// maximum of the offsets clamped to [0, M] (a broken offsets array then gives
+// no row to two experts, moves no access out of the tensors and makes no more
+// tiles than the host counted with), pref[e] the exclusive prefix of
+// ceil(rows / BQ).
 struct Experts {
   int* offs;
   int* pref;
@@ -155,12 +157,36 @@ __device__ __forceinline__ void setup_experts(const int32_t* __restrict__ offset
   // every wave scans all experts (kMaxExperts / 64 per lane at most); wave 0 writes
   const int lane = threadIdx.x & 63, per = (X.E + 63) / 64;
   const bool writer = threadIdx.x < 64;
+  auto clamped = [&](int e) { return min(max(offsets[e], 0), M); };
   int sum = 0;
+  bool falls = false;
   for (int j = 0; j < per; ++j) {
     const int e = lane * per + j;
     if (e >= X.E) break;
-    const int lo = min(max(offsets[e], 0), M), hi = max(lo, min(max(offsets[e + 1], 0), M));
-    sum += (hi - lo + BQ - 1) / BQ;
+    const int lo = clamped(e), hi = clamped(e + 1);
+    falls = falls || hi < lo;
+    sum += (max(hi, lo) - lo + BQ - 1) / BQ;
+  }
+  int top = 0;                          // the maximum of the lanes' before
+  if (__builtin_amdgcn_ballot_w64(falls) != 0) {
+    int most = 0;
+    for (int j = 0; j < per; ++j)
+      if (lane * per + j < X.E) most = max(most, clamped(lane * per + j));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(most, d, 64);
+      if (lane >= d) most = max(most, y);
+    }
+    top = __shfl_up(most, 1, 64);
+    if (lane == 0) top = 0;
+    sum = 0;
+    int lo = top;
+    for (int j = 0; j < per; ++j) {
+      const int e = lane * per + j;
+      if (e >= X.E) break;
+      lo = max(lo, clamped(e));
+      sum += (max(lo, clamped(e + 1)) - lo + BQ - 1) / BQ;
+    }
   }
   int incl = sum;
 #pragma unroll
@@ -170,11 +196,12 @@ __device__ __forceinline__ void setup_experts(const int32_t* __restrict__ offset
   }
   X.mtiles = __builtin_amdgcn_readlane(incl, 63);
   if (writer) {
-    int run = incl - sum;
+    int run = incl - sum, lo = top;
     for (int j = 0; j < per; ++j) {
       const int e = lane * per + j;
       if (e >= X.E) break;
-      const int lo = min(max(offsets[e], 0), M), hi = max(lo, min(max(offsets[e + 1], 0), M));
+      lo = max(lo, clamped(e));
+      const int hi = max(lo, clamped(e + 1));
       X.offs[e] = lo;
       X.pref[e] = run;
       run += (hi - lo + BQ - 1) / BQ;
