@@ -151,6 +151,18 @@ struct Experts {
   int E, mtiles;
 };
 
+// Inclusive scan over the wave's lanes (operands not negative, 0 neutral), by
+// row shifts: through LDS it takes 0.2 us more before a workgroup's first load.
+template <typename F>
+__device__ __forceinline__ int wave_scan(int x, F f) {
+  x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // rows: 1, 2, 4, 8 lanes below
+  x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));   // a row's last lane to the next row
+  return f(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+}
+
 template <int BQ>
 __device__ __forceinline__ void setup_experts(const int32_t* __restrict__ offsets, int M,
                                               Experts& X) {
@@ -159,24 +171,20 @@ __device__ __forceinline__ void setup_experts(const int32_t* __restrict__ offset
   const bool writer = threadIdx.x < 64;
   auto clamped = [&](int e) { return min(max(offsets[e], 0), M); };
   int sum = 0;
-  bool falls = false;
+  int least = 0;                        // below 0: an offset falls
   for (int j = 0; j < per; ++j) {
     const int e = lane * per + j;
     if (e >= X.E) break;
     const int lo = clamped(e), hi = clamped(e + 1);
-    falls = falls || hi < lo;
+    least = min(least, hi - lo);
     sum += (max(hi, lo) - lo + BQ - 1) / BQ;
   }
   int top = 0;                          // the maximum of the lanes' before
-  if (__builtin_amdgcn_ballot_w64(falls) != 0) {
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(least < 0) != 0, 0)) {
     int most = 0;
     for (int j = 0; j < per; ++j)
       if (lane * per + j < X.E) most = max(most, clamped(lane * per + j));
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(most, d, 64);
-      if (lane >= d) most = max(most, y);
-    }
+    most = wave_scan(most, [](int p, int q) { return max(p, q); });
     top = __shfl_up(most, 1, 64);
     if (lane == 0) top = 0;
     sum = 0;
@@ -188,12 +196,7 @@ __device__ __forceinline__ void setup_experts(const int32_t* __restrict__ offset
       sum += (max(lo, clamped(e + 1)) - lo + BQ - 1) / BQ;
     }
   }
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += y;
-  }
+  const int incl = wave_scan(sum, [](int p, int q) { return p + q; });
   X.mtiles = __builtin_amdgcn_readlane(incl, 63);
   if (writer) {
     int run = incl - sum, lo = top;
