@@ -399,9 +399,9 @@ mg_status mgemm_fwd_fp8(const void* x8, const float* x_scale, const void* w8, co
  *   DY[i, n] = e4m3(dy8[i, n]) dy_scale[n / 128, i],  W as for mgemm_fwd_fp8.
  * dy8: uint8 E4M3 codes [M, N]; dy_scale: fp32 [ceil(N/128), M]; dx: bf16
  * [M, K] (written).  Otherwise as mgemm_fwd_fp8.  M == 0 or K == 0 is a no-op;
- * N == 0 writes zeros.  The weight gradient of the same layer is kgemm_wgrad
- * on the bf16 rows: the fp8 products would cost its fp32 sums about 7 of
- * their 24 bits. */
+ * N == 0 writes zeros.  There is no weight gradient with these scales, which
+ * would need x and dy quantized along the tokens as well: the same layer's is
+ * kgemm_wgrad on the bf16 rows, or kgemm_wgrad_mx. */
 mg_status mgemm_dgrad_fp8(const void* dy8, const float* dy_scale, const void* w8,
                           const float* w_scale, const int32_t* offsets, void* dx, int64_t M,
                           int64_t N, int64_t K, int32_t E, int64_t max_m_per_e, void* stream);

@@ -896,9 +896,10 @@ void launch_tiled(bool dgrad, const Fp8Args& a, int64_t tiles, int64_t cap, hipS
 int launch_fp8(bool dgrad, const Fp8Args& a, int64_t max_m, hipStream_t s) {
   const int64_t pdim = dgrad ? a.K : a.N;
   const int64_t cus = device_cus();
-  // Which kernel: by the number of tiles that the rows give if they spread
-  // evenly (the host does not see the offsets; every expert's last tile is
-  // half full on average).  Results do not depend on the spread, only speed.
+  // Which kernel: by the number of tiles that the buffer's rows give if they
+  // spread evenly (the host does not see the offsets, nor how far the last of
+  // them lies below M; every expert's last tile is half full on average).
+  // Results do not depend on the spread, only speed.
   const int64_t live = a.E < a.M ? a.E : a.M;
   // Few rows: tiles of 32 rows.  With too few 128 x 128 tiles to fill the chip,
   // or too few rows to reuse a staged weight tile, a round of those is bound by

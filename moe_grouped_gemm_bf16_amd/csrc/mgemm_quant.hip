@@ -118,7 +118,10 @@ __device__ __forceinline__ uint32_t in_runs(uint32_t b, uint32_t blocks, uint32_
 // gathered rows, read again for every expert, do not get; 61 us with two rows
 // per wave in place of eight: 6.7 TB/s).  Where K is no multiple of 128 codes'
 // lines are shared by pieces, and a row's pieces go to one XCD (16384 x 6832:
-// 79 us without, 65 us with; at K = 4096 gathered rows 58 and 65 us).
+// 79 us without, 65 us with; where K is one, gathered rows lose: 32768 rows of
+// 4096 from 4096 tokens 49 us without, 57 us with).  Gathered rows are bound by
+// the vector unit (80% busy at K = 2048): a token's maximum and codes are formed
+// anew for each of its rows.
 constexpr int kBlocks = 4;
 
 template <typename T, bool SWI, bool GATHER>
