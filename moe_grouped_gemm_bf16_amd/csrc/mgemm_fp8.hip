@@ -643,26 +643,40 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_gemm_kernel(Fp8Args a) {
             odd |= factor_odd(s[j]);
           }
           if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd) != 0, 0)) {
-            // rows with an odd factor: the stage is added to them here, and with
-            // the factor 0 below (the check costs at most 1% where tiles are
-            // small: 8 experts, 512 rows each, N = 768, K = 2512: 24.9 -> 25.2 us)
+            // Rows with an odd factor: the stage is added to them here, and with
+            // the factor 0 below.  (The check costs at most 1% where tiles are
+            // small: 8 experts, 512 rows each, N = 768, K = 2512: 24.9 -> 25.2 us;
+            // such rows in every tile make it 45 us.)  A row of zero codes, whose
+            // scale is the quantizer's least and may make an odd factor with any
+            // small weight's, needs no sums.
+            uint32_t any = 0;
+#pragma unroll
+            for (int j = 0; j < C::MQ; ++j) {
+              uint32_t bits = 0;
+#pragma unroll
+              for (int w = 0; w < 8; ++w) bits |= (uint32_t)fq[j][w];
+              any |= factor_odd(s[j]) ? bits & 0x7F7F7F7Fu : 0u;
+            }
+            const bool sums = __builtin_amdgcn_ballot_w64(any != 0) != 0;
             Factor f[C::MQ];
 #pragma unroll
             for (int j = 0; j < C::MQ; ++j) {
               f[j] = factor_odd(s[j]) ? split_factor(rawq[j], raww, s[j]) : Factor{0.f, 1.f};
-              if (factor_odd(s[j])) s[j] = 0.f;
+              if (factor_odd(s[j])) s[j] = 0.f * f[j].m;     // (NaN of a scale that is none)
             }
+            if (sums) {
 #pragma unroll
-            for (int r = 0; r < C::MP; ++r) {
-              const i32x8 p = readP(st, r);
+              for (int r = 0; r < C::MP; ++r) {
+                const i32x8 p = readP(st, r);
 #pragma unroll
-              for (int j = 0; j < C::MQ; ++j) {
-                const f32x4 v = product(p, fq[j]);
+                for (int j = 0; j < C::MQ; ++j) {
+                  const f32x4 v = product(p, fq[j]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  acc[r][j][e] = __builtin_fmaf(v[e] * f[j].c, f[j].m, acc[r][j][e]);
-                // (one at a time: with more registers here the usual path is 2% slower)
-                __builtin_amdgcn_sched_barrier(0);
+                  for (int e = 0; e < 4; ++e)
+                    acc[r][j][e] = __builtin_fmaf(v[e] * f[j].c, f[j].m, acc[r][j][e]);
+                  // (one at a time: with more registers here the usual path is 2% slower)
+                  __builtin_amdgcn_sched_barrier(0);
+                }
               }
             }
           }

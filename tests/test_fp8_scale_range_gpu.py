@@ -90,3 +90,20 @@ def test_other_rows_do_not_depend_on_a_row_with_such_scales(sizes, dgrad):
     s = s.clone()
     s[0, :2], s[1, 2] = 2.0 ** -30, 1.0
     assert torch.equal(got[3:], f(q, s, w8, ws, off)[3:])
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("sizes", [[5, 0, 4], [150, 0, 133, 6], [3000, 0, 1100]])
+def test_rows_of_zeros_with_scales_out_of_range(sizes, dgrad):
+    """Zero codes (of either sign) give zero with any finite scale, and a scale
+    that is no number makes its row none, whatever the codes."""
+    print("[case] zero rows", sizes, dgrad, flush=True)
+    q, s, w8, ws, off = _operands(sizes, 8208, 656, dgrad, 10)
+    q[:5] = 0
+    q[1, ::3] = 0x80
+    s[:, 0], s[:, 1] = 3e38, 2.0 ** -100 / 448
+    s[0, 2], s[0, 3], s[0, 4] = 3e38, np.inf, np.nan
+    got = (mg.dgrad_fp8 if dgrad else mg.fwd_fp8)(q, s, w8, ws, off)
+    assert (got[:3] == 0).all() and torch.isnan(got[3:5]).all()
+    exact, mag = _exact(q, s, w8, ws, off, dgrad)
+    assert ((got[5:].double() - exact[5:]).abs() <= 2.0 ** -8 * exact[5:].abs() + 2.0 ** -10.8 * mag[5:] + 2.0 ** -134).all()
