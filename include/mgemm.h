@@ -228,6 +228,84 @@ mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float*
                            void* dlogits, int64_t T, int32_t E, int32_t k, int32_t normalize,
                            void* stream);
 
+/* Cross entropy of the output head, from hidden rows and the head's weights,
+ * without keeping the logits z[t, v] = sum_d x[t, d] w[v, d]:
+ *   lse[t]   = log sum_v exp(z[t, v])
+ *   logit[t] = z[t, targets[t] - first]   (0 where w has no such row)
+ *   loss[t]  = lse[t] - logit[t]
+ * x: bf16 [T, D]; w: bf16 [V, D], the vocabulary entries first .. first + V - 1;
+ * targets: int32 [T].  A token with a negative target does not count: its loss,
+ * lse and logit are 0, and no products are spent on it.  loss, lse, logit:
+ * fp32 [T] (written whole).  With the vocabulary in parts on several GPUs lse
+ * and logit are a part's: the whole's lse is the log-sum-exp of theirs, its
+ * logit their sum.  fp32 products and sums of exponentials, in a fixed order:
+ * bitwise reproducible.  An infinite or NaN logit makes NaN in its token's loss
+ * and no other's.
+ * D a multiple of 8, 8 <= D <= 2^20; V >= 1 of any size, T <= 2^22; the count of
+ * 256 x 128 tiles of z below 2^25, V D below 2^40; 0 <= first, first + V <= 2^31.  x, w 16-byte
+ * aligned, the others 4-byte.  workspace: mg_head_workspace(T, V, D) bytes of
+ * DEVICE memory, 16-byte aligned (no contents expected or kept); calls that may
+ * run at the same time need one each.  T == 0 is a no-op.  Allocates nothing. */
+mg_status mg_head_loss(const void* x, const void* w, const int32_t* targets, int64_t T, int64_t V,
+                       int64_t D, int64_t first, float* loss, float* lse, float* logit,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Distillation of the output head from a teacher's k top logits per token, at
+ * a temperature c = 1 / temperature:
+ *   q[t, j] = softmax over j of c teacher[t, j], over the entries that are there
+ *   lse[t]  = log sum_v exp(c z[t, v]),   logits[t, j] = z[t, index[t, j] - first]
+ *   loss[t] = sum_j q[t, j] (log q[t, j] + lse[t] - c logits[t, j])
+ * the divergence of softmax(c z) from q.  teacher: fp32 (teacher_bf16 == 0) or
+ * bf16 [T, k]; index: int32 [T, k], the entries' places in the vocabulary, in
+ * any order.  An entry with a negative index, or a teacher's value of -inf or
+ * NaN, is not there (+inf counts as the largest finite value); a token without
+ * entries does not count, as in mg_head_loss.  An index that is named twice has
+ * both entries' q.  logits: fp32 [T, k] (written whole, 0 where there is no entry
+ * or w has no such row); the loss takes them as they stand, so with the
+ * vocabulary in parts it is formed again from the joined lse and summed logits.
+ * 1 <= k <= 256, T k < 2^31; temperature positive and finite, as its inverse.
+ * Otherwise as mg_head_loss. */
+mg_status mg_head_distill(const void* x, const void* w, const void* teacher, int32_t teacher_bf16,
+                          const int32_t* index, int64_t T, int64_t V, int64_t D, int32_t k,
+                          int64_t first, float temperature, float* loss, float* lse, float* logits,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace of mg_head_loss and mg_head_distill (0 for sizes that
+ * they refuse). */
+int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
+
+/* Gradient of mg_head_loss to x and w, from upstream gradients dloss (fp32
+ * [T]) of the loss and dlse (fp32 [T], or NULL) of lse (a z loss):
+ *   dz[t, v] = (dloss[t] + dlse[t]) exp(z[t, v] - lse[t]) - dloss[t] [v = targets[t] - first]
+ *   dx = dz w,   dw = dz^T x
+ * lse: the forward's, or the whole vocabulary's where w is a part of it (dx is
+ * then a part of a sum).  dx: bf16 [T, D] (written whole, zeros for tokens that
+ * do not count) or NULL; dw: bf16 [V, D] (written whole) or NULL: a gradient
+ * that is not wanted costs nothing.  z is formed again, a piece of the
+ * vocabulary at a time; dz is rounded to bf16 once, relative to the largest of
+ * |dloss|, |dloss + dlse| (so that equal weights add no error of their own),
+ * the products accumulate in fp32 and are rounded once.  Bitwise reproducible.
+ * workspace: mg_head_bwd_workspace(T, V, D, 0) bytes.  T == 0 writes zero dw. */
+mg_status mg_head_loss_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
+                           const float* dloss, const float* dlse, int64_t T, int64_t V, int64_t D,
+                           int64_t first, void* dx, void* dw, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Gradient of mg_head_distill to x and w (the teacher gets none):
+ *   dz[t, v] = c dloss[t] (exp(c z[t, v] - lse[t]) - sum_j q[t, j] [v = index[t, j] - first])
+ * lse, logits: the forward's.  Otherwise as mg_head_loss_bwd; workspace:
+ * mg_head_bwd_workspace(T, V, D, k) bytes. */
+mg_status mg_head_distill_bwd(const void* x, const void* w, const void* teacher,
+                              int32_t teacher_bf16, const int32_t* index, const float* lse,
+                              const float* logits, const float* dloss, int64_t T, int64_t V,
+                              int64_t D, int32_t k, int64_t first, float temperature, void* dx,
+                              void* dw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace of the two gradients (k = 0: mg_head_loss_bwd; 0 for
+ * sizes that they refuse): about 2 GiB at most for T up to 65536 beside what
+ * grows with T D, dz being made for a piece of the vocabulary at a time. */
+int64_t mg_head_bwd_workspace(int64_t T, int64_t V, int64_t D, int32_t k);
+
 /* One group of mgemm_list: D [m, n] = A [m, k] B [n, k]^T (bf16 in and out,
  * fp32 accumulation, round to nearest even), row-major with row strides in
  * elements.  All three pointers are DEVICE pointers, 16-byte aligned; k, n and

@@ -12,6 +12,8 @@ kernels; PyTorch provides device memory and the current stream.
   grouped_list([(A_g, B_g), ...])   D_g = A_g B_g^T    independent GEMMs, per-group shapes
   moe_route(logits, k)    gate, row order, balance and z losses; moe_route_bwd, its gradient
   moe_combine(rows, token_rows, weights)               and moe_combine_bwd, its gradient
+  head_loss(x, w, targets)  cross entropy of the output head, no logits kept; head_loss_bwd
+  head_distill(x, w, teacher, index)  the same from a teacher's top logits; head_distill_bwd
   fwd_fp8, dgrad_fp8      block-scaled fp8 products on the codes of fp8_quantize,
       fp8_quantize_swiglu and fp8_quantize_weights
 
@@ -30,7 +32,8 @@ __all__ = ["fwd", "dgrad", "wgrad", "wgrad_noalloc", "fwd_swiglu", "dgrad_swiglu
            "moe_combine", "grouped_list", "list_descriptors", "grouped_list_desc",
            "mx_scales_blocked", "fwd_mx", "wgrad_mx", "wgrad_mx_tm", "fp8_quantize", "fp8_quantize_swiglu",
            "fp8_quantize_weights", "fwd_fp8", "dgrad_fp8", "Route", "moe_route", "moe_route_bwd",
-           "moe_combine_bwd", "Mgemm", "Kgemm",
+           "moe_combine_bwd", "HeadLoss", "head_loss", "head_loss_bwd", "HeadDistill",
+           "head_distill", "head_distill_bwd", "Mgemm", "Kgemm",
            "MgemmError", "status_str", "LIB"]
 
 
@@ -772,6 +775,168 @@ def moe_route_bwd(logits: torch.Tensor, weights: torch.Tensor, experts: torch.Te
          lse.data_ptr(), counts.data_ptr(), tokens.data_ptr(), _ptr(dweights), _ptr(dloss),
          out.data_ptr(), T, E, k, 1 if normalize else 0)
     return out
+
+
+class HeadLoss(NamedTuple):
+    """What head_loss computes, fp32 [T] each."""
+    loss: torch.Tensor        # lse - logit
+    lse: torch.Tensor         # log-sum-exp of the token's logits
+    logit: torch.Tensor       # logit of its target
+
+
+class HeadDistill(NamedTuple):
+    """What head_distill computes, in fp32."""
+    loss: torch.Tensor        # [T]     divergence from the teacher's entries
+    lse: torch.Tensor         # [T]     log-sum-exp of the token's logits / temperature
+    logits: torch.Tensor      # [T, k]  logits of the entries
+
+
+def _head(x: torch.Tensor, w: torch.Tensor, first: int) -> tuple:
+    _need(x, "x", torch.bfloat16, 2)
+    _need(w, "w", torch.bfloat16, 2)
+    T, D = x.shape
+    V, D2 = w.shape
+    if D2 != D:
+        raise ValueError(f"x is [T, {D}] but w is [V, {D2}]")
+    if first < 0 or first + V > 2 ** 31:
+        raise ValueError(f"vocabulary entries {first} .. {first + V - 1} are no int32 indices")
+    return T, V, D
+
+
+def _per_token(T: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t, name, torch.float32, 1)
+            if t.numel() != T:
+                raise ValueError(f"{name} must have {T} entries, got {t.numel()}")
+
+
+def _targets(targets: torch.Tensor, T: int) -> None:
+    _need(targets, "targets", torch.int32, 1)
+    if targets.numel() != T:
+        raise ValueError(f"targets must have {T} entries, got {targets.numel()}")
+
+
+def _teacher(teacher: torch.Tensor, index: torch.Tensor, T: int, temperature: float) -> int:
+    if not isinstance(teacher, torch.Tensor) or teacher.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("teacher must be a torch.float32 or torch.bfloat16 tensor")
+    _need(teacher, "teacher", teacher.dtype, 2)
+    _need(index, "index", torch.int32, 2)
+    k = index.shape[1]
+    if tuple(index.shape) != (T, k) or tuple(teacher.shape) != (T, k):
+        raise ValueError(f"teacher and index must be [{T}, k]")
+    if not 1 <= k <= 256:
+        raise ValueError(f"k must be in [1, 256], got {k}")
+    if not 0.0 < temperature < float("inf"):
+        raise ValueError(f"temperature must be positive and finite, got {temperature}")
+    return k
+
+
+def _head_grads(x, w, dx, dw, need_dx, need_dw, words):
+    """The gradients' tensors (None where not wanted) and the workspace."""
+    out = []
+    for name, like, t, need in (("dx", x, dx, need_dx), ("dw", w, dw, need_dw)):
+        if not need:
+            if t is not None:
+                raise ValueError(f"{name} is given but need_{name} is False")
+        elif t is None:
+            t = torch.empty_like(like)
+        else:
+            _need(t, name, torch.bfloat16, 2)
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must be {list(like.shape)}")
+        out.append(t)
+    _same_device(x.device, dx=out[0], dw=out[1])
+    return *out, torch.empty(words, dtype=torch.uint8, device=x.device)
+
+
+def head_loss(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, first: int = 0) -> HeadLoss:
+    """Cross entropy of the output head, without keeping the logits z = x w^T.
+
+    x bf16 [T, D], w bf16 [V, D] (D a multiple of 8, any V), targets int32 [T].
+    loss = lse - logit per token, lse = logsumexp(z), logit = z[target].  A
+    token with a negative target does not count: its loss, lse and logit are 0.
+    Where the vocabulary is spread over ranks, `first` is the index of w's row
+    0 and a target in another part has logit 0 here: with the parts' lse joined
+    (torch.logaddexp) and their logits summed, loss = lse - logit."""
+    T, V, D = _head(x, w, first)
+    _targets(targets, T)
+    _same_device(x.device, w=w, targets=targets)
+    loss, lse, logit = torch.empty(3 * T, dtype=torch.float32, device=x.device).split_with_sizes((T, T, T))
+    size = LIB.mg_head_workspace(T, V, D)
+    work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _run("mg_head_loss", x.device, x.data_ptr(), w.data_ptr(), targets.data_ptr(), T, V, D, int(first),
+         loss.data_ptr(), lse.data_ptr(), logit.data_ptr(), work.data_ptr(), size)
+    return HeadLoss(loss, lse, logit)
+
+
+def head_loss_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                  dloss: torch.Tensor, dlse: torch.Tensor | None = None, first: int = 0,
+                  dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                  need_dx: bool = True, need_dw: bool = True):
+    """Gradient of head_loss: (dx bf16 [T, D], dw bf16 [V, D]).
+
+    lse is the forward's (over ranks: the joined one; dx is then a part of a
+    sum).  dloss and dlse (fp32 [T]) are the gradients of loss and of lse (a z
+    loss on top: 2 c lse); tokens that do not count have none.  Either gradient
+    may be left out (need_dx, need_dw) and is None then."""
+    T, V, D = _head(x, w, first)
+    _targets(targets, T)
+    _per_token(T, lse=lse, dloss=dloss, dlse=dlse)
+    _same_device(x.device, w=w, targets=targets, lse=lse, dloss=dloss, dlse=dlse)
+    size = LIB.mg_head_bwd_workspace(T, V, D, 0)
+    dx, dw, work = _head_grads(x, w, dx, dw, need_dx, need_dw, size)
+    _run("mg_head_loss_bwd", x.device, x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+         dloss.data_ptr(), _ptr(dlse), T, V, D, int(first), _ptr(dx), _ptr(dw), work.data_ptr(), size)
+    return dx, dw
+
+
+def head_distill(x: torch.Tensor, w: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor,
+                 temperature: float = 1.0, first: int = 0) -> HeadDistill:
+    """Distillation of the output head from a teacher's k top logits per token.
+
+    teacher fp32 or bf16 [T, k], index int32 [T, k] (k <= 256): the teacher's
+    logits and their places in the vocabulary, -1 for no entry (a value of -inf
+    or NaN is none either).  q = softmax(teacher / temperature) over a token's
+    entries, loss = sum q (log q - log p) with p = softmax(z / temperature) over
+    the vocabulary; a token without entries has loss and lse 0.  `first` as in
+    head_loss: with joined lse and summed logits, loss = sum q (log q + lse -
+    logits / temperature)."""
+    T, V, D = _head(x, w, first)
+    k = _teacher(teacher, index, T, temperature)
+    _same_device(x.device, w=w, teacher=teacher, index=index)
+    loss, lse, logits = torch.empty((2 + k) * T, dtype=torch.float32,
+                                    device=x.device).split_with_sizes((T, T, T * k))
+    size = LIB.mg_head_workspace(T, V, D)
+    work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _run("mg_head_distill", x.device, x.data_ptr(), w.data_ptr(), teacher.data_ptr(),
+         1 if teacher.dtype == torch.bfloat16 else 0, index.data_ptr(), T, V, D, k, int(first),
+         float(temperature), loss.data_ptr(), lse.data_ptr(), logits.data_ptr(), work.data_ptr(), size)
+    return HeadDistill(loss, lse, logits.view(T, k))
+
+
+def head_distill_bwd(x: torch.Tensor, w: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor,
+                     lse: torch.Tensor, logits: torch.Tensor, dloss: torch.Tensor,
+                     temperature: float = 1.0, first: int = 0, dx: torch.Tensor | None = None,
+                     dw: torch.Tensor | None = None, need_dx: bool = True, need_dw: bool = True):
+    """Gradient of head_distill: (dx bf16 [T, D], dw bf16 [V, D]).
+
+    lse and logits are the forward's, dloss (fp32 [T]) the gradient of its
+    loss; the teacher gets none.  Otherwise as head_loss_bwd."""
+    T, V, D = _head(x, w, first)
+    k = _teacher(teacher, index, T, temperature)
+    _per_token(T, lse=lse, dloss=dloss)
+    _need(logits, "logits", torch.float32, 2)
+    if tuple(logits.shape) != (T, k):
+        raise ValueError(f"logits must be [{T}, {k}]")
+    _same_device(x.device, w=w, teacher=teacher, index=index, lse=lse, logits=logits, dloss=dloss)
+    size = LIB.mg_head_bwd_workspace(T, V, D, k)
+    dx, dw, work = _head_grads(x, w, dx, dw, need_dx, need_dw, size)
+    _run("mg_head_distill_bwd", x.device, x.data_ptr(), w.data_ptr(), teacher.data_ptr(),
+         1 if teacher.dtype == torch.bfloat16 else 0, index.data_ptr(), lse.data_ptr(),
+         logits.data_ptr(), dloss.data_ptr(), T, V, D, k, int(first), float(temperature), _ptr(dx),
+         _ptr(dw), work.data_ptr(), size)
+    return dx, dw
 
 
 def Mgemm(x: torch.Tensor, w: torch.Tensor, cnt: torch.Tensor, max_M_per_E: int = 0,

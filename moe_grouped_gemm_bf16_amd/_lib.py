@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmgemm.so
 MG_OK, MG_ERR_NULL, MG_ERR_SHAPE, MG_ERR_ALIGN, MG_ERR_DEVICE, MG_ERR_LAUNCH, MG_ERR_OFFSETS = range(7)
 
 # name -> (restype, argtypes); the exported symbols of include/mgemm.h
-_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "mgemm_fwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i64, _vp]),
     "mgemm_dgrad": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i64, _vp]),
@@ -41,6 +41,15 @@ SIGNATURES = {
     "mg_moe_route_workspace": (_i64, [_i64, _i32]),
     "mg_moe_route_bwd": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
                                 _i32, _vp]),
+    "mg_head_loss": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "mg_head_loss_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp,
+                                _i64, _vp]),
+    "mg_head_distill": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _i32, _i64, _f32, _vp, _vp,
+                               _vp, _vp, _i64, _vp]),
+    "mg_head_distill_bwd": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                   _i64, _f32, _vp, _vp, _vp, _i64, _vp]),
+    "mg_head_workspace": (_i64, [_i64, _i64, _i64]),
+    "mg_head_bwd_workspace": (_i64, [_i64, _i64, _i64, _i32]),
     "mg_check_rows_host": (_i32, [_vp, _i64, _i64]),
     "mg_check_list_host": (_i32, [_vp, _i32]),
     "mg_status_str": (ctypes.c_char_p, [_i32]),

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmgemm.so")
 SOURCES = ["mgemm_kernels.hip", "mgemm_combine.hip", "mgemm_fp8.hip", "mgemm_quant.hip",
-           "mgemm_route.hip", "mgemm_api.cpp"]
+           "mgemm_route.hip", "mgemm_head.hip", "mgemm_api.cpp"]
 PROBE_LIB = os.path.join(PKG, "libmgemm_probe.so")
 PROBE_SOURCES = ["mgemm_probe.hip"]
 

@@ -508,6 +508,139 @@ mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float*
 
 namespace {
 
+bool head_sizes(int64_t T, int64_t V, int64_t D, int64_t k) {
+  return T >= 0 && T <= (int64_t(1) << 22) && V >= 1 && V <= kMaxRows && D >= 8 &&
+         D <= (int64_t(1) << 20) && (D & 7) == 0 && k >= 0 && k <= 256 && T * k <= kMaxRows &&
+         ((T + 127) / 128) * ((V + 255) / 256) < (int64_t(1) << 25) && V * D < (int64_t(1) << 40);
+}
+
+// Checks that the four calls share; k == 0: a target per token, `index` holds them.
+mg_status check_head(const mg::HeadArgs& a, const int32_t* index, int64_t k, int64_t need,
+                     int64_t workspace_bytes) {
+  if (!head_sizes(a.T, a.V, a.D, k) || a.first < 0 || a.first > kMaxRows + 1 - a.V)
+    return MG_ERR_SHAPE;
+  // (no NaN, no inverse that is not a normal number)
+  if (!(a.inv_temperature >= 1.17549435e-38f && a.inv_temperature <= 3.4e38f)) return MG_ERR_SHAPE;
+  if (a.T == 0) return MG_OK;
+  if (workspace_bytes < need) return MG_ERR_SHAPE;
+  if (!a.x || !a.w || !index || (k > 0 && !a.teacher) || !a.workspace) return MG_ERR_NULL;
+  if (!aligned16(a.x) || !aligned16(a.w) || !aligned16(a.workspace) || misaligned4(index) ||
+      (reinterpret_cast<uintptr_t>(a.teacher) & (a.teacher_bf16 ? 1u : 3u)))
+    return MG_ERR_ALIGN;
+  return MG_OK;
+}
+
+mg_status head_forward(mg::HeadArgs& a, const int32_t* index, int64_t k, float* loss, float* lse,
+                       float* logits, void* workspace, int64_t workspace_bytes, void* stream) {
+  a.workspace = workspace;
+  mg_status st = check_head(a, index, k, mg_head_workspace(a.T, a.V, a.D), workspace_bytes);
+  if (st != MG_OK) return st;
+  if (a.T == 0) return MG_OK;
+  if (!loss || !lse || !logits) return MG_ERR_NULL;
+  if (misaligned4(loss) || misaligned4(lse) || misaligned4(logits)) return MG_ERR_ALIGN;
+  if ((st = check_device()) != MG_OK) return st;
+  a.loss = loss;
+  a.lse = lse;
+  a.logits = logits;
+  return mg::launch_head(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MG_OK : MG_ERR_LAUNCH;
+}
+
+mg_status head_backward(mg::HeadArgs& a, const int32_t* index, int64_t k, const float* lse,
+                        const float* logits, const float* dloss, const float* dlse, void* dx,
+                        void* dw, void* workspace, int64_t workspace_bytes, void* stream) {
+  a.workspace = workspace;
+  mg_status st = check_head(a, index, k, mg_head_bwd_workspace(a.T, a.V, a.D, (int32_t)k),
+                            workspace_bytes);
+  if (st != MG_OK) return st;
+  if ((!dx && !dw) || (a.T == 0 && !dw)) return MG_OK;
+  if (!aligned16(dx) || !aligned16(dw)) return MG_ERR_ALIGN;
+  if (a.T > 0) {
+    if (!lse || !dloss || (k > 0 && !logits)) return MG_ERR_NULL;
+    if (misaligned4(lse) || misaligned4(logits) || misaligned4(dloss) || misaligned4(dlse))
+      return MG_ERR_ALIGN;
+  }
+  if ((st = check_device()) != MG_OK) return st;
+  a.lse_in = lse;
+  a.logits_in = logits;
+  a.dloss = dloss;
+  a.dlse = dlse;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw = static_cast<uint16_t*>(dw);
+  return mg::launch_head_bwd(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MG_OK
+                                                                               : MG_ERR_LAUNCH;
+}
+
+mg::HeadArgs head_args(const void* x, const void* w, int64_t T, int64_t V, int64_t D, int64_t first) {
+  mg::HeadArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.T = T; a.V = V; a.D = D; a.first = first;
+  a.inv_temperature = 1.f;
+  return a;
+}
+
+mg::HeadArgs distill_args(const void* x, const void* w, const void* teacher, int32_t teacher_bf16,
+                          const int32_t* index, int64_t T, int64_t V, int64_t D, int32_t k,
+                          int64_t first, float temperature) {
+  mg::HeadArgs a = head_args(x, w, T, V, D, first);
+  a.teacher = teacher;
+  a.teacher_bf16 = teacher_bf16 ? 1 : 0;
+  a.index = index;
+  a.k = k;
+  a.inv_temperature = 1.f / temperature;
+  return a;
+}
+
+}  // namespace
+
+int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D) {
+  return head_sizes(T, V, D, 0) && T > 0 ? mg::head_workspace_bytes(T, V, D) : 0;
+}
+
+int64_t mg_head_bwd_workspace(int64_t T, int64_t V, int64_t D, int32_t k) {
+  return head_sizes(T, V, D, k) && T > 0 ? mg::head_bwd_workspace_bytes(T, V, D, k) : 0;
+}
+
+mg_status mg_head_loss(const void* x, const void* w, const int32_t* targets, int64_t T, int64_t V,
+                       int64_t D, int64_t first, float* loss, float* lse, float* logit,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  mg::HeadArgs a = head_args(x, w, T, V, D, first);
+  a.targets = targets;
+  return head_forward(a, targets, 0, loss, lse, logit, workspace, workspace_bytes, stream);
+}
+
+mg_status mg_head_loss_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
+                           const float* dloss, const float* dlse, int64_t T, int64_t V, int64_t D,
+                           int64_t first, void* dx, void* dw, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  mg::HeadArgs a = head_args(x, w, T, V, D, first);
+  a.targets = targets;
+  return head_backward(a, targets, 0, lse, nullptr, dloss, dlse, dx, dw, workspace, workspace_bytes,
+                       stream);
+}
+
+mg_status mg_head_distill(const void* x, const void* w, const void* teacher, int32_t teacher_bf16,
+                          const int32_t* index, int64_t T, int64_t V, int64_t D, int32_t k,
+                          int64_t first, float temperature, float* loss, float* lse, float* logits,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+  if (k < 1) return MG_ERR_SHAPE;
+  mg::HeadArgs a = distill_args(x, w, teacher, teacher_bf16, index, T, V, D, k, first, temperature);
+  return head_forward(a, index, k, loss, lse, logits, workspace, workspace_bytes, stream);
+}
+
+mg_status mg_head_distill_bwd(const void* x, const void* w, const void* teacher,
+                              int32_t teacher_bf16, const int32_t* index, const float* lse,
+                              const float* logits, const float* dloss, int64_t T, int64_t V,
+                              int64_t D, int32_t k, int64_t first, float temperature, void* dx,
+                              void* dw, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (k < 1) return MG_ERR_SHAPE;
+  mg::HeadArgs a = distill_args(x, w, teacher, teacher_bf16, index, T, V, D, k, first, temperature);
+  return head_backward(a, index, k, lse, logits, dloss, nullptr, dx, dw, workspace, workspace_bytes,
+                       stream);
+}
+
+namespace {
+
 // Shared body of the two row quantizers; `swiglu`: x holds g | u of 2 K columns.
 mg_status fp8_rows(bool swiglu, const void* x, int32_t x_fp32, const int32_t* gather,
                    const int32_t* offsets, void* codes, float* scales, int64_t M, int64_t T,

@@ -140,6 +140,34 @@ int launch_moe_combine_bwd(const uint16_t* dout, const uint16_t* rows, const int
                            const float* weights, uint16_t* drows, float* dweights, int64_t M,
                            int64_t T, int32_t k, int64_t D, hipStream_t s);
 
+// Losses of the output head: cross entropy (targets) or distillation (teacher,
+// index), and their gradients (see mg_head_loss and mg_head_distill).
+struct HeadArgs {
+  const uint16_t* x;          // [T, D] bf16
+  const uint16_t* w;          // [V, D] bf16
+  int64_t T, V, D;
+  int64_t first;              // vocabulary index of w's row 0
+  const int32_t* targets;     // [T], cross entropy
+  const void* teacher;        // [T, k] fp32 or bf16, distillation
+  const int32_t* index;       // [T, k], or NULL: cross entropy
+  int32_t k, teacher_bf16;
+  float inv_temperature;      // 1 for cross entropy
+  float* loss;                // forward: [T]
+  float* lse;                 // [T]
+  float* logits;              // [T] or [T, k]
+  const float* lse_in;        // backward: the forward's
+  const float* logits_in;     // [T, k]
+  const float* dloss;         // [T]
+  const float* dlse;          // [T] or NULL
+  uint16_t* dx;               // [T, D] bf16 or NULL
+  uint16_t* dw;               // [V, D] bf16 or NULL
+  void* workspace;
+};
+int64_t head_workspace_bytes(int64_t T, int64_t V, int64_t D);
+int64_t head_bwd_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t k);
+int launch_head(const HeadArgs& a, hipStream_t s);
+int launch_head_bwd(const HeadArgs& a, hipStream_t s);
+
 // Where the weight gradient's token split takes its workspace from.
 enum WsKind {
   kWsStream = 0,   // a device allocation per (device, stream), made on first use
