@@ -235,7 +235,7 @@ mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float*
  *   loss[t]  = lse[t] - logit[t]
  * x: bf16 [T, D]; w: bf16 [V, D], the vocabulary entries first .. first + V - 1;
  * targets: int32 [T].  A token with a negative target does not count: its loss,
- * lse and logit are 0, and no products are spent on it.  loss, lse, logit:
+ * lse and logit are 0 (in a batch of more than 256 it costs no products).  loss, lse, logit:
  * fp32 [T] (written whole).  With the vocabulary in parts on several GPUs lse
  * and logit are a part's: the whole's lse is the log-sum-exp of theirs, its
  * logit their sum.  fp32 products and sums of exponentials, in a fixed order:
@@ -263,7 +263,7 @@ mg_status mg_head_loss(const void* x, const void* w, const int32_t* targets, int
  * both entries' q.  logits: fp32 [T, k] (written whole, 0 where there is no entry
  * or w has no such row); the loss takes them as they stand, so with the
  * vocabulary in parts it is formed again from the joined lse and summed logits.
- * 1 <= k <= 256, T k < 2^31; temperature positive and finite, as its inverse.
+ * 1 <= k <= 256, T k < 2^31; 1e-37 <= temperature <= 1e37.
  * Otherwise as mg_head_loss. */
 mg_status mg_head_distill(const void* x, const void* w, const void* teacher, int32_t teacher_bf16,
                           const int32_t* index, int64_t T, int64_t V, int64_t D, int32_t k,

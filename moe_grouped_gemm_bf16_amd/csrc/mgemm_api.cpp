@@ -519,8 +519,8 @@ mg_status check_head(const mg::HeadArgs& a, const int32_t* index, int64_t k, int
                      int64_t workspace_bytes) {
   if (!head_sizes(a.T, a.V, a.D, k) || a.first < 0 || a.first > kMaxRows + 1 - a.V)
     return MG_ERR_SHAPE;
-  // (no NaN, no inverse that is not a normal number)
-  if (!(a.inv_temperature >= 1.17549435e-38f && a.inv_temperature <= 3.4e38f)) return MG_ERR_SHAPE;
+  // (no NaN; a factor that is a normal number)
+  if (!(a.c >= 1e-37 && a.c <= 1e37)) return MG_ERR_SHAPE;
   if (a.T == 0) return MG_OK;
   if (workspace_bytes < need) return MG_ERR_SHAPE;
   if (!a.x || !a.w || !index || (k > 0 && !a.teacher) || !a.workspace) return MG_ERR_NULL;
@@ -570,12 +570,18 @@ mg_status head_backward(mg::HeadArgs& a, const int32_t* index, int64_t k, const 
                                                                                : MG_ERR_LAUNCH;
 }
 
+void head_temperature(mg::HeadArgs& a, double temperature) {
+  a.c = 1.0 / temperature;
+  a.scale = (float)(a.c * 1.44269504088896340736);
+  a.unscale = a.c / (double)a.scale;
+}
+
 mg::HeadArgs head_args(const void* x, const void* w, int64_t T, int64_t V, int64_t D, int64_t first) {
   mg::HeadArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.w = static_cast<const uint16_t*>(w);
   a.T = T; a.V = V; a.D = D; a.first = first;
-  a.inv_temperature = 1.f;
+  head_temperature(a, 1.0);
   return a;
 }
 
@@ -587,7 +593,7 @@ mg::HeadArgs distill_args(const void* x, const void* w, const void* teacher, int
   a.teacher_bf16 = teacher_bf16 ? 1 : 0;
   a.index = index;
   a.k = k;
-  a.inv_temperature = 1.f / temperature;
+  head_temperature(a, temperature);
   return a;
 }
 

@@ -8,17 +8,18 @@
 //   dz[t, v] = a[t] p[t, v] - sum over the entries at v of their weights b q,
 //   p = exp(c z - lse),   dx = dz w,   dw = dz^T x,
 // three matrix products of 2 T D V operations backward (z again, since it was
-// not kept) against one forward.  All four run on one kernel, nt_kernel below:
-// C[q, p] = sum_r Q[q, r] P[p, r] with both operands contiguous along r.
+// not kept) against one forward.  All run on one kernel, nt_kernel below, as
+// C[q, p] = sum_r Q[q, r] P[p, r]:
 //   logits (forward, backward)  P = w rows, Q = x rows, r = hidden column
-//   input gradient              P = dz rows (tokens), Q = w^T rows, r = vocabulary
-//   weight gradient             P = dz^T rows (vocabulary), Q = x^T rows, r = token
+//   input gradient              P = dz rows (tokens), Q = w columns, r = vocabulary
+//   weight gradient             P = dz columns (vocabulary), Q = x columns, r = token
 // The forward's epilogue turns a tile of logits into one (maximum, sum of
-// exponentials) per token and 128 vocabulary entries; the backward's turns it
-// into dz, in 16 bits, for a piece of the vocabulary at a time.  dz, its
-// transpose and the transposes of x and of w's piece lie in panels of 64
-// reduction steps, [r / 64][row][64]: a staged row is 128 contiguous bytes and
-// a tile's rows follow each other, whatever the widths.
+// exponentials) per token and 64 or 128 vocabulary entries; the backward's turns
+// it into dz, in 16 bits, for a piece of the vocabulary at a time.  dz lies in
+// panels of 64 vocabulary entries, [v / 64][token][64]: whether a product reads
+// it along the vocabulary or along the tokens, it reads 128 contiguous bytes.
+// Operands that are strided along r (w and x as the gradients read them, dz in
+// the weight gradient) are staged as they lie and transposed by the LDS read.
 //
 // Tokens that do not count (no target, no teacher's entry) are left out before
 // the products: rows[] lists the others, x is packed by it (not if all count).
@@ -42,8 +43,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) const bf16x8 lds_frag;
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kOOB = 0x80000000u;       // offset bit past any buffer range
 
 // 128-bit raw buffer descriptor: loads past `bytes` return zero.
@@ -77,12 +76,13 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// One operand of a product: row i at base + i stride, reduction step k at
-// (k / 64) kstep + 2 (k % 64) of the row.
+// One operand of a product, rows of `stride` bytes, each in blocks of 64 values
+// `step` bytes apart.  Its rows are the product's rows and the values its
+// reduction steps, or (strided, below) the other way round.
 struct Operand {
   const void* base;
-  uint32_t stride;      // bytes between rows
-  uint32_t kstep;       // bytes between blocks of 64 reduction steps
+  uint32_t stride;
+  uint32_t step;
 };
 
 // A token that counts, as the backward's epilogue takes it.
@@ -95,25 +95,33 @@ struct Token {
 
 enum { kStats = 0, kDz = 1, kDx = 2, kDw = 3 };
 
+// How a product's tiles are cut, by the number of tokens that count.
+struct Plan {
+  int32_t small;        // 256 x 128 tiles, not 256 x 256
+  int32_t splits;       // parts of the reduction (input gradient)
+};
+
 struct NtArgs {
   Operand P, Q;
-  const void* Q_all;        // logits: x itself, taken when all tokens count
-  const int32_t* n;         // device: tokens that count
+  const void* Q_all;        // x itself, taken when all tokens count
+  const int32_t* n;         // device: tokens that count, NULL: all
+  const Plan* plan_at;      // device, NULL: `plan`
+  Plan plan;
   int32_t np, nq, K;        // rows of P and of Q and reduction steps; those that are
-                            // tokens hold their upper bound
-  int32_t tokens;           // that bound: T
-  int32_t first;            // logits: vocabulary entry of P's row 0
+                            // tokens hold T
+  int32_t tokens;           // T
   int32_t gq;               // tiles along Q that run beside each other
-  int32_t splits;           // input gradient: parts of the reduction
   int32_t add;              // input gradient: add to what is there
+  int32_t first;            // logits: vocabulary entry of P's row 0 ...
+  int64_t target_first;     // ... and, of targets[], of w's row 0
   float scale;              // logits: c log2(e)
-  float2* part;             // forward: [2 tiles along P][T] (maximum, sum)
+  float2* part;             // forward: [parts][T] (maximum, sum), base 2
   float* logit;             // forward: logit of a token's target, or NULL
-  const Token* token;       // logits: per counting token
+  const Token* token;       // logits: per counting token, or
+  const int32_t* targets;   // (forward of all tokens) its target
   const float* top;         // backward: [2], largest |a|, |b| and its inverse
-  uint16_t* dz;             // [V' / 64][T'][64] (or NULL: not wanted)
-  uint16_t* dzt;            // [T' / 64][V'][64] (or NULL)
-  int64_t rows_t, rows_v;   // T', V' of these
+  uint16_t* dz;             // [V' / 64][T'][64]
+  int64_t rows_t;           // T'
   float* dx;                // [splits][T'][D] fp32
   uint16_t* dw;             // [V, D]
   int32_t D;
@@ -121,11 +129,11 @@ struct NtArgs {
 
 // Tile of BP x BQ outputs, WP x WQ waves of (64 MH) x 64 each, 64 reduction
 // steps a stage, two stages in LDS.  Every operand tile is staged as two
-// units, the rows of the waves' first halves and those of their second, so a
-// stage is the four products of a P half and a Q half, and a unit can be
-// refilled as soon as its fragments are in registers, while the rest of the
-// stage is still multiplied: a load has five of the eight phases of two stages
-// (about 1.3 us of 256 x 256 tiles) before its data are read.
+// units, its first half and its second; a wave holds 32 MH rows of each P half
+// and 32 of each Q half.  So a stage is four products of a P half and a Q half,
+// and a unit can be refilled as soon as its fragments are in registers, while
+// the rest of the stage is still multiplied: a load has five of the eight
+// phases of two stages (1.3 us of 256 x 256 tiles) before its data are read.
 template <int MH_, int WP_, int WQ_>
 struct Cfg {
   static constexpr int MH = MH_, WP = WP_, WQ = WQ_;
@@ -139,107 +147,165 @@ struct Cfg {
 typedef Cfg<2, 2, 4> Large;      // 256 x 256
 typedef Cfg<1, 4, 2> Small;      // 256 x 128
 
-template <class C>
-struct Core {
-  f32x16 acc[2 * C::MH][2];
-  bf16x8 A0[C::MH][4], A1[C::MH][4], B0[4], B1[4];
-  uint32_t aP[4], aQ[4];               // fragment addresses by slice of 16 steps
-  uint32_t rowP, rowQ, maxP, maxQ, chunk;
-  uint64_t baseP, baseQ;
-  uint32_t lds0, live;
-  uint32_t strideP, strideQ, kstepP, kstepQ;
-  int wave, K, kd;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-  // LDS rows of 128 bytes in 16-byte chunks; chunk c of row r lies at c ^ (r % 8),
-  // so 32 rows read at one chunk touch every bank group equally often.
-  __device__ __forceinline__ void init(const NtArgs& a, int K_, char* lds) {
-    const int lane = threadIdx.x & 63;
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
-    const int wp = wave / C::WQ, wq = wave % C::WQ, l32 = lane & 31, h = lane >> 5;
+// One operand of the tile: N waves along it, each with M blocks of 32 rows in
+// either half; B waves' worth of LDS at `lds`.
+// RS (strided): the unit holds [64 reduction steps][32 M N] values as they lie
+// in memory and a fragment is read by the LDS transpose loads: lane i of 16
+// addresses step i / 4 and values 4 (i % 4) .. + 3 and receives value i of four
+// steps.  Otherwise [32 M N rows][64 steps], read with 128-bit loads.
+// Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) of its eight;
+// strided, at c ^ 4 (row % 4) of 16, or c ^ 4 (row / 2 % 2) of eight, so that
+// the four steps of a transpose load lie in different quarters of the banks.
+template <bool RS, int M, int N>
+struct Side {
+  static constexpr int U = 32 * M * N;          // rows (strided: values) of a unit
+  static constexpr int BYTES = U * 128;
+  static constexpr int S = U / 64;              // loads of a unit per wave
+  static constexpr int kReads = RS ? 8 * M : 4 * M;
+  static_assert(U == 128 || U == 64, "row swizzle");
+  uint32_t at[RS ? M : 4];     // fragment addresses, by block or by slice of 16 steps
+  uint32_t lds;                // the operand's first unit
+  uint32_t row, chunk;         // load: byte offset of the lane's row; its chunk's bytes
+  uint64_t base;
+  uint32_t stride, step, most; // most: offset of the last row (strided: valid values)
+  int first;                   // strided: step of the lane in a stage
+
+  __device__ __forceinline__ void init(const Operand& o, uint32_t lds_, int w, int wave, int lane) {
+    lds = lds_;
+    stride = o.stride;
+    step = o.step;
+    const int l32 = lane & 31, h = lane >> 5;
+    if constexpr (RS) {
+      const int i = lane & 15, g = (lane >> 4) & 1, r = 8 * h + (i >> 2);
+      const int swz = U == 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t c = (uint32_t)(((2 * kk + h) ^ (l32 & 7)) << 4);
-      aP[kk] = lds0 + (uint32_t)((wp * 32 * C::MH + l32) * 128) + c;
-      aQ[kk] = lds0 + (uint32_t)(4 * C::UP) + (uint32_t)((wq * 32 + l32) * 128) + c;
+      for (int b = 0; b < M; ++b) {
+        const int c = (4 * (w * M + b) + 2 * g + ((i & 3) >> 1)) ^ swz;
+        at[b] = lds + (uint32_t)(r * U * 2 + 16 * c + 8 * (i & 1));
+      }
+      constexpr int kRow = U / 8;                              // chunks of a row
+      const int lr = lane / kRow;                              // row within 1 KiB
+      first = 64 / kRow * (wave * S) + lr;
+      row = (uint32_t)first * stride;
+      chunk = 16u * (uint32_t)((lane % kRow) ^ (U == 128 ? 4 * (lr & 3) : 4 * ((lr >> 1) & 1)));
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        at[kk] = lds + (uint32_t)((w * 32 * M + l32) * 128) + (uint32_t)(((2 * kk + h) ^ (l32 & 7)) << 4);
+      row = (uint32_t)(8 * S * wave + (lane >> 3)) * stride;
+      chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7)) << 4);
     }
-    K = K_;
-    strideP = a.P.stride;
-    strideQ = a.Q.stride;
-    kstepP = a.P.kstep;
-    kstepQ = a.Q.kstep;
-    // row of a unit -> row of the tile: half h of wave w holds rows
-    // (2 w + h) 32 MH .. of P, (2 w + h) 32 .. of Q
-    const int uP = 8 * C::SP * wave + (lane >> 3), uQ = 8 * C::SQ * wave + (lane >> 3);
-    rowP = (uint32_t)((uP / (32 * C::MH)) * 64 * C::MH + uP % (32 * C::MH)) * strideP;
-    rowQ = (uint32_t)((uQ / 32) * 64 + uQ % 32) * strideQ;
-    chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7)) << 4);
   }
+  // Rows from o0 of n, steps from k0 (a multiple of 128).  Rows past the end
+  // repeat the last one (their results are not stored); strided, values past it
+  // are zeros.
+  __device__ __forceinline__ void source(const void* p, int o0, int n, int k0) {
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    if constexpr (RS) {
+      base = b + (uint64_t)(o0 >> 6) * step + (uint64_t)k0 * stride;
+      most = (uint32_t)min(2 * U, n - o0);
+    } else {
+      base = b + (uint64_t)o0 * stride + (uint64_t)(k0 >> 6) * step;
+      most = (uint32_t)(min(2 * U, n - o0) - 1) * stride;
+    }
+  }
+  __device__ __forceinline__ void advance() { base += RS ? 128 * (uint64_t)stride : 2 * (uint64_t)step; }
 
-  // The tile whose stages the next loads bring: rows from p0 of np, q0 of nq,
-  // steps from k0.  Rows past the end repeat the last one (their results are
-  // not stored), steps past the end are zeros.  Without a tile nothing is read.
-  __device__ __forceinline__ void source(const NtArgs& a, const void* Q, bool live_, int p0, int np,
-                                         int q0, int nq, int k0, int K_) {
-    maxP = (uint32_t)(min(C::BP, np - p0) - 1) * strideP;
-    maxQ = (uint32_t)(min(C::BQ, nq - q0) - 1) * strideQ;
-    baseP = reinterpret_cast<uint64_t>(a.P.base) + (uint64_t)p0 * strideP + (uint64_t)(k0 >> 6) * kstepP;
-    baseQ = reinterpret_cast<uint64_t>(Q) + (uint64_t)q0 * strideQ + (uint64_t)(k0 >> 6) * kstepQ;
-    live = live_ ? 0x7fffffffu : 0u;
-    K = K_;
-    kd = 0;
-  }
-  __device__ __forceinline__ void advance() {
-    baseP += 2 * (uint64_t)kstepP;
-    baseQ += 2 * (uint64_t)kstepQ;
-    kd += 128;
-  }
-
-  template <bool IsQ, int HALF, int BUF>
-  __device__ __forceinline__ void load() {
-    constexpr int S = IsQ ? C::SQ : C::SP;
-    const i32x4 rsrc = make_rsrc(reinterpret_cast<const void*>(IsQ ? baseQ : baseP), live);
-    const bool in = (int)(chunk >> 1) + kd + BUF * 64 < K;
+  // Refill of a unit with a stage, `left` steps of the reduction being left at
+  // the buffer pair's start.  Steps past the end are zeros.
+  template <int HALF, int BUF>
+  __device__ __forceinline__ void load(uint32_t live, int left, int wave) const {
+    const i32x4 rsrc = make_rsrc(reinterpret_cast<const void*>(base), live);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      // segment s of the wave: 8 unit rows further
-      const uint32_t add = (uint32_t)(8 * s + (IsQ ? 32 : 32 * C::MH) * HALF) * (IsQ ? strideQ : strideP);
-      const uint32_t r = min((IsQ ? rowQ : rowP) + add, IsQ ? maxQ : maxP);
-      const uint32_t off = (r + chunk + BUF * (IsQ ? kstepQ : kstepP)) | (in ? 0u : kOOB);
-      dma16(rsrc, lds0 + (IsQ ? 4u * C::UP + (2u * BUF + HALF) * C::UQ : (2u * BUF + HALF) * C::UP) +
-                      (uint32_t)(wave * S + s) * 1024u, off);
+      uint32_t off;
+      if constexpr (RS) {
+        constexpr int kRows = 512 / U;                         // steps of a load
+        const uint32_t col = chunk >> 1;                       // value in the unit
+        off = row + (uint32_t)(BUF * 64 + kRows * s) * stride +
+              (col >> 6) * step + HALF * (U / 64) * step + 2 * (col & 63);
+        off |= first + BUF * 64 + kRows * s < left && HALF * U + col < most ? 0u : kOOB;
+      } else {
+        off = min(row + (uint32_t)(8 * s + U * HALF) * stride, most) + chunk + BUF * step;
+        off |= (int)(chunk >> 1) + BUF * 64 < left ? 0u : kOOB;
+      }
+      dma16(rsrc, lds + (2u * BUF + HALF) * BYTES + (uint32_t)(wave * S + s) * 1024u, off);
     }
   }
   template <int HALF, int BUF>
-  __device__ __forceinline__ void readP(bf16x8 (&f)[C::MH][4]) {
+  __device__ __forceinline__ void read(bf16x8 (&f)[M][4]) const {
+    constexpr uint32_t unit = (2 * BUF + HALF) * BYTES;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int i = 0; i < C::MH; ++i)
-        f[i][kk] = *(lds_frag*)(uintptr_t)(aP[kk] + (2 * BUF + HALF) * C::UP + i * 4096);
+      for (int b = 0; b < M; ++b) {
+        if constexpr (RS) {
+          const uint32_t a = at[b] + unit + kk * 16 * U * 2;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + 4 * U * 2));
+          f[b][kk] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+          f[b][kk] = *(lds_frag*)(uintptr_t)(at[kk] + unit + b * 4096);
+        }
+      }
+  }
+};
+
+template <class C, bool PRS, bool QRS>
+struct Core {
+  f32x16 acc[2 * C::MH][2];
+  bf16x8 A0[C::MH][4], A1[C::MH][4], B0[1][4], B1[1][4];
+  Side<PRS, C::MH, C::WP> P;
+  Side<QRS, 1, C::WQ> Q;
+  uint32_t live;
+  int wave, left;
+
+  __device__ __forceinline__ void init(const NtArgs& a, char* lds) {
+    const int lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
+    P.init(a.P, lds0, wave / C::WQ, wave, lane);
+    Q.init(a.Q, lds0 + 4 * C::UP, wave % C::WQ, wave, lane);
+  }
+  // The tile that the next loads bring; without one they read nothing.
+  __device__ __forceinline__ void source(const void* p, const void* q, bool live_, int p0, int np, int q0,
+                                         int nq, int k0, int K) {
+    P.source(p, p0, np, k0);
+    Q.source(q, q0, nq, k0);
+    live = live_ ? 0x7fffffffu : 0u;
+    left = K - k0;
+  }
+  __device__ __forceinline__ void advance() {
+    P.advance();
+    Q.advance();
+    left -= 128;
   }
   template <int HALF, int BUF>
-  __device__ __forceinline__ void readQ(bf16x8 (&f)[4]) {
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      f[kk] = *(lds_frag*)(uintptr_t)(aQ[kk] + (2 * BUF + HALF) * C::UQ);
-  }
+  __device__ __forceinline__ void loadP() const { P.template load<HALF, BUF>(live, left, wave); }
+  template <int HALF, int BUF>
+  __device__ __forceinline__ void loadQ() const { Q.template load<HALF, BUF>(live, left, wave); }
+
   template <int HP, int HQ>
-  __device__ __forceinline__ void mul(const bf16x8 (&A)[C::MH][4], const bf16x8 (&B)[4]) {
+  __device__ __forceinline__ void mul(const bf16x8 (&A)[C::MH][4], const bf16x8 (&B)[1][4]) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int i = 0; i < C::MH; ++i)
         acc[C::MH * HP + i][HQ] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            A[i][kk], B[kk], acc[C::MH * HP + i][HQ], 0, 0, 0);
+            A[i][kk], B[0][kk], acc[C::MH * HP + i][HQ], 0, 0, 0);
   }
-  // Reads between the products, one for one.
+  // The reads between the products, evenly.
   template <int R>
   __device__ __forceinline__ void mix() {
+    constexpr int n = 4 * C::MH, each = (R + n - 1) / n;
 #pragma unroll
-    for (int i = 0; i < 4 * C::MH; ++i) {
+    for (int i = 0; i < n; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (i < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i * each < R) __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -264,11 +330,11 @@ struct Core {
       for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
   }
   __device__ __forceinline__ void start() {
-    load<false, 0, 0>(); load<true, 0, 0>(); load<true, 1, 0>(); load<false, 1, 0>();
-    load<false, 0, 1>(); load<true, 1, 1>(); load<true, 0, 1>(); load<false, 1, 1>();
+    loadP<0, 0>(); loadQ<0, 0>(); loadQ<1, 0>(); loadP<1, 0>();
+    loadP<0, 1>(); loadQ<1, 1>(); loadQ<0, 1>(); loadP<1, 1>();
     edge<3 * C::SP + 3 * C::SQ>();
-    readP<0, 0>(A0);
-    readQ<0, 0>(B0);
+    P.template read<0, 0>(A0);
+    Q.template read<0, 0>(B0);
     edge<kFlight>();
     advance();
   }
@@ -276,15 +342,15 @@ struct Core {
   // half that a later phase needs into registers that are free, and refills
   // the unit that was read two phases before (of the stages 128 steps on).
   __device__ __forceinline__ void pair() {
-    constexpr int RP = 4 * C::MH, RQ = 4;
-    load<false, 0, 0>(); readQ<1, 0>(B1); mul<0, 0>(A0, B0); mix<RQ>();
-    load<true, 0, 0>();  readP<1, 0>(A1); mul<0, 1>(A0, B1); mix<RP>(); edge<kFlight>();
-    load<true, 1, 0>();  readP<0, 1>(A0); mul<1, 1>(A1, B1); mix<RP>();
-    load<false, 1, 0>(); readQ<1, 1>(B1); mul<1, 0>(A1, B0); mix<RQ>(); edge<kFlight>();
-    load<false, 0, 1>(); readQ<0, 1>(B0); mul<0, 1>(A0, B1); mix<RQ>();
-    load<true, 1, 1>();  readP<1, 1>(A1); mul<0, 0>(A0, B0); mix<RP>(); edge<kFlight>();
-    load<true, 0, 1>();  readP<0, 0>(A0); mul<1, 0>(A1, B0); mix<RP>();
-    load<false, 1, 1>(); readQ<0, 0>(B0); mul<1, 1>(A1, B1); mix<RQ>(); edge<kFlight>();
+    constexpr int RP = decltype(P)::kReads, RQ = decltype(Q)::kReads;
+    loadP<0, 0>(); Q.template read<1, 0>(B1); mul<0, 0>(A0, B0); mix<RQ>();
+    loadQ<0, 0>(); P.template read<1, 0>(A1); mul<0, 1>(A0, B1); mix<RP>(); edge<kFlight>();
+    loadQ<1, 0>(); P.template read<0, 1>(A0); mul<1, 1>(A1, B1); mix<RP>();
+    loadP<1, 0>(); Q.template read<1, 1>(B1); mul<1, 0>(A1, B0); mix<RQ>(); edge<kFlight>();
+    loadP<0, 1>(); Q.template read<0, 1>(B0); mul<0, 1>(A0, B1); mix<RQ>();
+    loadQ<1, 1>(); P.template read<1, 1>(A1); mul<0, 0>(A0, B0); mix<RP>(); edge<kFlight>();
+    loadQ<0, 1>(); P.template read<0, 0>(A0); mul<1, 0>(A1, B0); mix<RP>();
+    loadP<1, 1>(); Q.template read<0, 0>(B0); mul<1, 1>(A1, B1); mix<RQ>(); edge<kFlight>();
     advance();
   }
 };
@@ -332,39 +398,37 @@ __device__ __forceinline__ Item item_of(int id, int tp, int tq, int gq) {
 // XCD has a contiguous range of tiles, gq of them along Q at a time, that
 // share operand rows in its L2.
 template <int EPI, class C>
-__global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
-  extern __shared__ char lds[];
-  const int n_tok = a.n != nullptr ? __builtin_amdgcn_readfirstlane(*a.n) : a.tokens;
+__device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const int n_tok, char* lds) {
+  constexpr bool kLogits = EPI == kStats || EPI == kDz;
   const int np = EPI == kDx ? n_tok : a.np;
-  const int nq = EPI == kStats || EPI == kDz ? n_tok : a.nq;
-  const int K = EPI == kDw ? (n_tok + 7) & ~7 : a.K;
+  const int nq = kLogits ? n_tok : a.nq;
+  const int K = EPI == kDw ? n_tok : a.K;
   const int tp = (np + C::BP - 1) / C::BP, tq = (nq + C::BQ - 1) / C::BQ;
   // pairs of stages; an empty reduction takes one of zeros
   const int pairs = max(1, (K + 127) >> 7);
-  const int splits = EPI == kDx ? min(a.splits, pairs) : 1;
+  const int splits = EPI == kDx ? min(plan.splits, pairs) : 1;
   const int total = tp * tq * splits, xcd = blockIdx.x & 7, wgs = gridDim.x >> 3;
   const int per = total >> 3, rem = total & 7;
   int id = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
   const int end = xcd * per + min(xcd, rem) + per + (xcd < rem ? 1 : 0);
   if (id >= end) return;
-  const void* Q = (EPI == kStats || EPI == kDz) && n_tok == a.tokens ? a.Q_all : a.Q.base;
+  const void* Qp = EPI != kDx && n_tok == a.tokens ? a.Q_all : a.Q.base;
 
-  Core<C> c;
-  c.init(a, K, lds);
+  Core<C, EPI == kDw, !kLogits> c;
+  c.init(a, lds);
   auto range = [&](const Item& t, int& k0, int& m) {     // pairs [k0, k0 + m) of the item
+    k0 = 0;
+    m = pairs;
     if (EPI == kDx) {
       const int each = pairs / splits, more = pairs - each * splits;
       k0 = t.s * each + min(t.s, more);
       m = each + (t.s < more ? 1 : 0);
-    } else {
-      k0 = 0;
-      m = pairs;
     }
   };
   auto aim = [&](const Item& t, bool live) {
     int k0, m;
     range(t, k0, m);
-    c.source(a, Q, live, t.ip * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K - 128 * k0);
+    c.source(a.P.base, Qp, live, t.ip * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
     return m;
   };
   Item t = item_of(id, tp, tq, a.gq), ahead = t;
@@ -374,6 +438,9 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wp = c.wave / C::WQ, wq = c.wave % C::WQ;
   constexpr int MP = 2 * C::MH;
+  // acc[i][j][4 g + e]: row P_ROW(i) + 8 g + 4 h + e of the wave's pw.., Q row
+  // qw + 32 wq + l32 + BQ / 2 j
+  auto p_row = [](int i) { return i / C::MH * (C::BP / 2) + 32 * (i % C::MH); };
 
   while (true) {
     int k0, m;
@@ -389,34 +456,44 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
       c.pair();
       --left;
     }
-    // acc[i][j][4 g + e]: P row 32 i + 8 g + 4 h + e, Q row 32 j + l32 of the wave's part
-    const int pw = t.ip * C::BP + wp * 32 * MP, qw = t.iq * C::BQ + wq * 64;
+    const int pw = t.ip * C::BP + wp * 32 * C::MH, qw = t.iq * C::BQ + wq * 32;
 
     if constexpr (EPI == kStats) {
       if (t.ip * C::BP + C::BP > np) {
+        const int rows = np - pw - 4 * h;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
           for (int g = 0; g < 16; ++g)
-            if (pw + 32 * i + 8 * (g >> 2) + 4 * h + (g & 3) >= np) {
+            if (p_row(i) + 8 * (g >> 2) + (g & 3) >= rows) {
               c.acc[i][0][g] = -INFINITY;
               c.acc[i][1][g] = -INFINITY;
             }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int q = qw + 32 * j + l32;
+        const int q = qw + C::BQ / 2 * j + l32;
         if (a.logit != nullptr) {
-          const int at = q < nq ? a.token[q].target - pw : -1;
-          if (__builtin_amdgcn_ballot_w64(at >= 0 && at < 32 * MP) != 0) {
-            const int rel = at - 4 * h;
+          int at = -1;
+          if (q < nq) {
+            if (a.targets != nullptr) {
+              const int64_t v = (int64_t)a.targets[q] - a.target_first;
+              at = v >= 0 && v < np ? (int)v : -1;
+            } else {
+              at = a.token[q].target;
+            }
+          }
+          const int rel = at - pw;
+          const bool here = at >= 0 && rel >= 0 && rel < C::BP && ((rel >> 2) & 1) == h &&
+                            rel % (C::BP / 2) < 32 * C::MH;
+          if (__builtin_amdgcn_ballot_w64(here) != 0) {
             float z = 0.f;
 #pragma unroll
             for (int i = 0; i < MP; ++i)
 #pragma unroll
               for (int g = 0; g < 16; ++g)
-                z = rel == 32 * i + 8 * (g >> 2) + (g & 3) ? c.acc[i][j][g] : z;
-            if (at >= 0 && at < 32 * MP && ((at >> 2) & 1) == h) a.logit[q] = z;
+                z = rel - 4 * h == p_row(i) + 8 * (g >> 2) + (g & 3) ? c.acc[i][j][g] : z;
+            if (here) a.logit[q] = z;
           }
         }
         float top = c.acc[0][j][0];
@@ -436,8 +513,7 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
           }
         s0 += s1;
         s0 += __shfl_xor(s0, 32);
-        if (h == 0 && q < nq)
-          a.part[(int64_t)(t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
+        if (h == 0 && q < nq) a.part[(int64_t)(t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
       }
     }
 
@@ -446,16 +522,13 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
       const float inv = a.top[1];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int q = qw + 32 * j + l32;
+        const int q = qw + C::BQ / 2 * j + l32;
         Token tk = {INFINITY, 0.f, 0.f, -1};
         if (q < nq) tk = a.token[q];
         const float wa = tk.a * inv, wb = tk.b * inv;
-        const int at = tk.target < 0 ? -1 : tk.target - a.first - pw;
-        const bool told = __builtin_amdgcn_ballot_w64(at >= 0 && at < 32 * MP) != 0;
-        // 32 x 64 values of a wave are 64 panel rows of 128 bytes in either order
-        char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)(pw >> 6) * a.rows_t + q) * 128 + 8 * h;
-        char* dzt = reinterpret_cast<char*>(a.dzt) +
-                    ((int64_t)(qw >> 6) * a.rows_v + pw + 4 * h + (lane & 3)) * 128 + 64 * j + 2 * (l32 & ~3);
+        const int rel = tk.target < 0 ? -1 : tk.target - a.first - pw;
+        const bool told = __builtin_amdgcn_ballot_w64(rel >= 0 && rel < C::BP) != 0;
+        char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)(pw >> 6) * a.rows_t + q) * 128 + 2 * (pw & 63) + 8 * h;
 #pragma unroll
         for (int i = 0; i < MP; ++i) {
           f32x16 v;
@@ -464,22 +537,20 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
             v[g] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][g], a.scale, -tk.lse2));
           if (told) {
 #pragma unroll
-            for (int g = 0; g < 16; ++g) v[g] -= at - 4 * h == 32 * i + 8 * (g >> 2) + (g & 3) ? wb : 0.f;
+            for (int g = 0; g < 16; ++g) v[g] -= rel - 4 * h == p_row(i) + 8 * (g >> 2) + (g & 3) ? wb : 0.f;
           }
           if (edge_p) {
 #pragma unroll
-            for (int g = 0; g < 16; ++g) v[g] = 32 * i + 8 * (g >> 2) + (g & 3) < np - pw - 4 * h ? v[g] : 0.f;
+            for (int g = 0; g < 16; ++g)
+              v[g] = p_row(i) + 8 * (g >> 2) + (g & 3) < np - pw - 4 * h ? v[g] : 0.f;
           }
+          if (i == C::MH) dz += C::BP / 128 * a.rows_t * 128;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            // the one rounding of dz: 16-bit operands of the two products
-            const uint32_t lo = pack2(v[4 * g], v[4 * g + 1]), hi = pack2(v[4 * g + 2], v[4 * g + 3]);
-            if (a.dz != nullptr) *reinterpret_cast<u32x2*>(dz + 64 * (i & 1) + 16 * g) = u32x2{lo, hi};
-            if (a.dzt != nullptr)
-              *reinterpret_cast<u32x2*>(dzt + 1024 * g) = quad_transpose(lo, hi, lane);
+            // the one rounding of dz: a 16-bit operand of the two products
+            *reinterpret_cast<u32x2*>(dz + 64 * (i % C::MH) + 16 * g) =
+                u32x2{pack2(v[4 * g], v[4 * g + 1]), pack2(v[4 * g + 2], v[4 * g + 3])};
           }
-          if (i & 1) dz += a.rows_t * 128;
-          dzt += 4096;
           __builtin_amdgcn_sched_barrier(0);      // a block's values at a time: registers
         }
       }
@@ -490,21 +561,22 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
       auto store = [&](auto whole, auto add) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int d = qw + 32 * j + l32;
+          const int d = qw + C::BQ / 2 * j + l32;
           const int rows = d < nq ? np - pw - 4 * h : 0;
           float* to = a.dx + ((int64_t)t.s * a.rows_t + pw + 4 * h) * a.D + d;
 #pragma unroll
           for (int i = 0; i < MP; ++i) {
             asm volatile("" : "+v"(to));      // a block's addresses at a time: registers
+            float* at = to + (int64_t)p_row(i) * a.D;
 #pragma unroll
             for (int g = 0; g < 16; ++g) {
-              if (whole.value || 32 * i + 8 * (g >> 2) + (g & 3) < rows) {
+              if (whole.value || p_row(i) + 8 * (g >> 2) + (g & 3) < rows) {
                 // (adding: once per element and launch, so there is no order to
                 // depend on, and no load to wait for)
-                if (add.value) unsafeAtomicAdd(to, c.acc[i][j][g]);
-                else *to = c.acc[i][j][g];
+                if (add.value) unsafeAtomicAdd(at, c.acc[i][j][g]);
+                else *at = c.acc[i][j][g];
               }
-              to += (g & 3) == 3 ? 5 * (int64_t)a.D : a.D;
+              at += (g & 3) == 3 ? 5 * (int64_t)a.D : a.D;
             }
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -521,7 +593,7 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
       const float scale = a.top[0];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int d = qw + 32 * j + (l32 & ~3);
+        const int d = qw + C::BQ / 2 * j + (l32 & ~3);
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
@@ -529,7 +601,7 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
             const u32x2 v = quad_transpose(
                 pack2(c.acc[i][j][4 * g] * scale, c.acc[i][j][4 * g + 1] * scale),
                 pack2(c.acc[i][j][4 * g + 2] * scale, c.acc[i][j][4 * g + 3] * scale), lane);
-            const int p = pw + 32 * i + 8 * g + 4 * h + (lane & 3);
+            const int p = pw + p_row(i) + 8 * g + 4 * h + (lane & 3);
             if (p < np && d < nq) *reinterpret_cast<u32x2*>(a.dw + (int64_t)p * a.D + d) = v;
           }
       }
@@ -540,6 +612,19 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
     t = ahead;
   }
   wait_vm<0>();       // the loads in flight write this workgroup's LDS
+}
+
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
+  extern __shared__ char lds[];
+  const int n = a.n != nullptr ? __builtin_amdgcn_readfirstlane(*a.n) : a.tokens;
+  Plan plan = a.plan;
+  if (a.plan_at != nullptr) {
+    plan.small = __builtin_amdgcn_readfirstlane(a.plan_at->small);
+    plan.splits = __builtin_amdgcn_readfirstlane(a.plan_at->splits);
+  }
+  if (plan.small) products<EPI, Small>(a, plan, n, lds);
+  else products<EPI, Large>(a, plan, n, lds);
 }
 
 // ------------------------------------------------------------ token passes --
@@ -583,7 +668,7 @@ __device__ __forceinline__ bool teacher_row(const HeadArgs& a, int64_t t, int la
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
-    lq[i] = at[i] >= 0 ? (lq[i] - top) * a.inv_temperature : -INFINITY;
+    lq[i] = at[i] >= 0 ? (lq[i] - top) * (float)a.c : -INFINITY;
     q[i] = at[i] >= 0 ? expf(lq[i]) : 0.f;
     sum += q[i];
   }
@@ -615,11 +700,44 @@ __global__ __launch_bounds__(256) void head_counts_kernel(const HeadArgs a, int3
   if (lane == 0) pos[t] = counts ? 0 : -1;
 }
 
+// The time of a product's tiles, in ns: rounds of the chip's 256 compute units,
+// each of a tile's pairs of stages and its epilogue; for a split reduction the
+// parts' way through memory besides.  Measured: TIMES.
+__host__ __device__ __forceinline__ int64_t tile_time(bool small, int64_t np, int64_t nq, int64_t pairs,
+                                                      int64_t splits, int64_t out) {
+  const int64_t tiles = ((np + 255) / 256) * (small ? (nq + 127) / 128 : (nq + 255) / 256) * splits;
+  const int64_t rounds = (tiles + 255) / 256, each = (pairs + splits - 1) / splits;
+  return rounds * (small ? 1350 * each + 3000 : 2400 * each + 5000) + (splits > 1 ? splits * out / 640 : 0);
+}
+
+// The quicker of the two tile sizes and of up to `most` parts.
+__host__ __device__ __forceinline__ Plan plan_of(int64_t np, int64_t nq, int64_t K, int most, int64_t out) {
+  const int64_t pairs = K > 128 ? (K + 127) / 128 : 1;
+  Plan best = {0, 1};
+  int64_t least = tile_time(false, np, nq, pairs, 1, out);
+  for (int i = 1; i < 24; ++i) {
+    // parts 1, 2, 3, 4, 6, 8, 12, .. 64
+    const int k = i >> 1, s = k < 2 ? k + 1 : (k & 1 ? 4 : 3) << (k - 2) / 2;
+    if (s > most) break;
+    const int64_t t = tile_time(i & 1, np, nq, pairs, s, out);
+    if (t < least) {
+      least = t;
+      best.small = i & 1;
+      best.splits = s;
+    }
+  }
+  return best;
+}
+
+// Plans of a call's products.
+enum { kPlanLogits = 0, kPlanDx = 1, kPlanDw = 2, kPlans = 3 };
+
 // The counting tokens in order: pos[t] becomes a token's place (-1 for none),
 // rows[place] its token, n their number; per place what the epilogues need,
-// and, backward, the largest weight.  One workgroup.
+// the products' plans and, backward, the largest weight.  One workgroup.
 __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, int32_t* pos, int32_t* rows,
-                                                          int32_t* n, Token* token, float* top) {
+                                                          int32_t* n, Token* token, Plan* plans, int64_t piece,
+                                                          int32_t splits, float* top) {
   __shared__ int counts[16];
   __shared__ float tops[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -646,8 +764,8 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, int3
         k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
       }
       if (a.dloss != nullptr) {
-        k.lse2 = a.lse_in[t] * kLog2e;
-        k.b = a.dloss[t] * a.inv_temperature;
+        k.lse2 = (float)((double)a.lse_in[t] / a.unscale);
+        k.b = a.dloss[t] * (float)a.c;
         k.a = a.dlse != nullptr ? k.b + a.dlse[t] : k.b;
         most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
       }
@@ -657,7 +775,11 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, int3
     __syncthreads();
   }
   if (threadIdx.x == 0) *n = base;
+  // (a thread for each, on waves of their own)
+  if (threadIdx.x == 64) plans[kPlanLogits] = plan_of(piece, base, a.D, 1, 0);
   if (top == nullptr) return;
+  if (threadIdx.x == 128) plans[kPlanDx] = plan_of(base, a.D, piece, splits, (int64_t)base * a.D);
+  if (threadIdx.x == 192) plans[kPlanDw] = plan_of(piece, a.D, base, 1, 0);
   most = wave_max(most);
   if (lane == 0) tops[wave] = most;
   __syncthreads();
@@ -683,80 +805,52 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const uint16_t* x, const
   }
 }
 
-// Panels of the transpose: out[r / 64][c][r % 64] = in[row(r)][c], zeros for
-// r past the end of its panel's valid rows.  rows: row(r) = rows[r], or NULL.
-// n: valid rows on the device, or NULL for `count`.  One workgroup per 64 rows
-// and 128 columns.
-__global__ __launch_bounds__(256) void head_transpose_kernel(const uint16_t* in, const int32_t* rows,
-                                                             const int32_t* n, int32_t count, int32_t D,
-                                                             uint16_t* out) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[64][128 + 8];
-  const int valid = n != nullptr ? *n : count;
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 128;
-  if (r0 >= valid) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = threadIdx.x + 256 * i, r = s >> 4, c = 8 * (s & 15);
-    u32x4 v = {0, 0, 0, 0};
-    if (r0 + r < valid && c0 + c < D) {
-      const int64_t row = rows != nullptr ? rows[r0 + r] : r0 + r;
-      v = *reinterpret_cast<const u32x4*>(in + row * D + c0 + c);
-    }
-    *reinterpret_cast<u32x4*>(&tile[r][c]) = v;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = threadIdx.x + 256 * i, c = s >> 3, r = 8 * (s & 7);
-    if (c0 + c >= D) continue;
-    u32x4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = (uint32_t)tile[r + 2 * e][c] | (uint32_t)tile[r + 2 * e + 1][c] << 16;
-    *reinterpret_cast<u32x4*>(out + ((int64_t)blockIdx.x * D + c0 + c) * 64 + r) = v;
-  }
-}
-
-// lse of every token from its parts, and the loss of a target.  64 tokens per
-// workgroup of 16 waves, a lane per token, the parts dealt to the waves.
-__global__ __launch_bounds__(1024) void head_join_kernel(const HeadArgs a, const int32_t* pos,
-                                                         const float2* part, int32_t parts,
-                                                         const float* logit) {
-  __shared__ float2 got[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 64 + lane;
-  const int p = t < a.T ? pos[t] : -1;
+// lse of every token from its parts, and the loss of a target.  TT tokens per
+// workgroup of NT threads, NT / TT threads to a token's parts.  The sum's
+// logarithm, the reference and the difference from the logit are put together
+// in 64 bits: each is up to log V, their sum may be far smaller.
+template <int TT, int NT>
+__global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const int32_t* pos, const Plan* plan_at,
+                                                       const Plan plan, const float2* part,
+                                                       const float* logit, double* lse64) {
+  __shared__ float2 got[NT / 64][TT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = threadIdx.x % TT;
+  const int64_t t = (int64_t)blockIdx.x * TT + tok;
+  const int small = plan_at != nullptr ? plan_at->small : plan.small;
+  const int parts = (int)((a.V + 255) / 256) * (small ? Small::WP : Large::WP);
+  int p = -1;
+  if (t < a.T) p = pos != nullptr ? pos[t] : a.index != nullptr || a.targets[t] >= 0 ? (int)t : -1;
   float top = -INFINITY, sum = 0.f;
-  if (p >= 0)
-    for (int i = wave; i < parts; i += 16) {
-      const float2 v = part[(int64_t)i * a.T + p];
-      const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
-      sum = sum * exp2f(top - ref) + v.y * exp2f(v.x - ref);
-      top = m;
-    }
-  got[wave][lane] = make_float2(top, sum);
-  __syncthreads();
-  if (wave != 0 || t >= a.T) return;
-  for (int w = 1; w < 16; ++w) {
-    const float2 v = got[w][lane];
+  auto join = [&](const float2 v) {
     const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
-    sum = sum * exp2f(top - ref) + v.y * exp2f(v.x - ref);
+    sum = sum * __builtin_amdgcn_exp2f(top - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
     top = m;
+  };
+  if (p >= 0) {
+#pragma unroll 4
+    for (int i = threadIdx.x / TT; i < parts; i += NT / TT) join(part[(int64_t)i * a.T + p]);
   }
-  const float lse = p >= 0 ? kLn2 * (top + log2f(sum)) : 0.f;
-  a.lse[t] = lse;
-  if (a.index == nullptr) {
+#pragma unroll
+  for (int d = TT; d < 64; d <<= 1) join(make_float2(__shfl_xor(top, d), __shfl_xor(sum, d)));
+  if (lane < TT) got[wave][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x >= TT || t >= a.T) return;
+  for (int w = 1; w < NT / 64; ++w) join(got[w][threadIdx.x]);
+  const double lse = p >= 0 ? (double)top * a.unscale + log((double)sum) : 0.0;
+  a.lse[t] = (float)lse;
+  if (a.index != nullptr) {
+    lse64[t] = lse;
+  } else {
     const int64_t at = (int64_t)a.targets[t] - a.first;
     const float z = p >= 0 && at >= 0 && at < a.V ? logit[p] : 0.f;
     a.logits[t] = z;
-    a.loss[t] = lse - z;
+    a.loss[t] = (float)(lse - (double)z);
   }
 }
 
 // Distillation: the logits of a token's entries and its loss.  One wave per
-// token; 8 columns per lane and step.
-__global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a) {
+// token, four entries at a time, 8 columns per lane and step.
+__global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a, const double* lse64) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.T) return;
@@ -767,33 +861,56 @@ __global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a) {
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
     z[i] = 0.f;
-    for (int j = 0; j < 64 && 64 * i + j < a.k; ++j) {
-      const int v = __builtin_amdgcn_readlane(at[i], j) ;
-      if (v < a.first || v - a.first >= a.V) continue;
-      const uint16_t* w = a.w + (int64_t)(v - a.first) * a.D;
-      float s = 0.f;
-      for (int d = 8 * lane; d < a.D; d += 512) {
-        const u32x4 xv = *reinterpret_cast<const u32x4*>(x + d), wv = *reinterpret_cast<const u32x4*>(w + d);
+    // the entry's row of w, -1 where it has none here
+    const int64_t rel = at[i] < 0 ? -1 : (int64_t)at[i] - a.first;
+    const int row = rel >= 0 && rel < a.V ? (int)rel : -1;
+    uint64_t todo = __builtin_amdgcn_ballot_w64(row >= 0);
+    while (todo != 0) {
+      int j[4], r[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s = __builtin_fmaf(__uint_as_float(xv[e] << 16), __uint_as_float(wv[e] << 16), s);
-          s = __builtin_fmaf(__uint_as_float(xv[e] & 0xffff0000u), __uint_as_float(wv[e] & 0xffff0000u), s);
+      for (int e = 0; e < 4; ++e) {
+        j[e] = todo != 0 ? __builtin_ctzll(todo) : j[0];      // (past the last one: the first again)
+        todo &= todo - 1;
+        r[e] = __builtin_amdgcn_readlane(row, j[e]);
+      }
+      float s[4] = {};
+#pragma unroll 2
+      for (int d = 8 * lane; d < a.D; d += 512) {
+        const u32x4 xv = *reinterpret_cast<const u32x4*>(x + d);
+        u32x4 wv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wv[e] = *reinterpret_cast<const u32x4*>(a.w + (int64_t)r[e] * a.D + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float lo = __uint_as_float(xv[c] << 16), hi = __uint_as_float(xv[c] & 0xffff0000u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[e] = __builtin_fmaf(lo, __uint_as_float(wv[e][c] << 16), s[e]);
+            s[e] = __builtin_fmaf(hi, __uint_as_float(wv[e][c] & 0xffff0000u), s[e]);
+          }
         }
       }
-      s = wave_sum(s);
-      if (lane == j) z[i] = s;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = wave_sum(s[e]);
+        if (lane == j[e]) z[i] = s[e];
+      }
     }
   }
-  float loss = 0.f;
-  const float lse = any ? a.lse[t] : 0.f;
+  double loss = 0.0;
+  const double lse = any ? lse64[t] : 0.0;
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
     const int j = 64 * i + lane;
     if (j < a.k) a.logits[t * a.k + j] = z[i];
-    if (any && q[i] > 0.f) loss += q[i] * (lq[i] + lse - z[i] * a.inv_temperature);
+    if (any && q[i] > 0.f) loss += (double)q[i] * ((double)lq[i] + (lse - (double)z[i] * a.c));
   }
-  loss = wave_sum(loss);
-  if (lane == 0) a.loss[t] = loss;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) loss += __shfl_xor(loss, d);
+  if (lane == 0) {
+    a.loss[t] = (float)loss;
+    if (!any) a.lse[t] = 0.f;
+  }
 }
 
 // Distillation, backward: dz at the entries of a token, from their logits.
@@ -836,7 +953,7 @@ __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a
     if (any && at[i] >= 0 && !early[i] && at[i] >= a.first && at[i] - a.first < a.V) {
       where = (int)(at[i] - a.first);
       const Token k = token[p];
-      const float pr = exp2f(__builtin_fmaf(a.logits_in[t * a.k + j], a.inv_temperature * kLog2e, -k.lse2));
+      const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[t * a.k + j], a.scale, -k.lse2));
       bits = pack2(k.a * top[1] * pr - k.b * top[1] * sum[i], 0.f) & 0xffffu;
     }
     entry[t * a.k + j] = where;
@@ -844,27 +961,26 @@ __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a
   }
 }
 
-// These values into the piece [v0, v0 + count) of dz and of its transpose.
+// These values into the piece [v0, v0 + count) of dz.
 __global__ __launch_bounds__(256) void head_entry_store_kernel(const int32_t* pos, const int32_t* entry,
                                                                const uint16_t* value, int64_t total,
                                                                int32_t k, int32_t v0, int32_t count,
-                                                               int64_t rows_t, int64_t rows_v,
-                                                               uint16_t* dz, uint16_t* dzt) {
+                                                               int64_t rows_t, uint16_t* dz) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int v = entry[i];
     if (v < v0 || v - v0 >= count) continue;
     const int64_t p = pos[i / k], c = v - v0;
-    if (dz != nullptr) dz[((c >> 6) * rows_t + p) * 64 + (c & 63)] = value[i];
-    if (dzt != nullptr) dzt[((p >> 6) * rows_v + c) * 64 + (p & 63)] = value[i];
+    dz[((c >> 6) * rows_t + p) * 64 + (c & 63)] = value[i];
   }
 }
 
 // dx[t] = top sum over the parts of dx32[part][place], one rounding; zeros for
 // tokens that do not count.  A thread per 8 columns.
 __global__ __launch_bounds__(256) void head_dx_kernel(const int32_t* pos, const float* dx32,
-                                                      int32_t splits, int64_t rows_t, int64_t T,
-                                                      int32_t D, const float* top, uint16_t* dx) {
+                                                      const Plan* plan, int32_t pairs, int64_t rows_t,
+                                                      int64_t T, int32_t D, const float* top, uint16_t* dx) {
   const int64_t total = T * (D / 8);
+  const int splits = min(plan->splits, pairs);
   const float scale = top[0];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t t = i / (D / 8);
@@ -912,6 +1028,7 @@ struct Common {
   int32_t* pos;
   int32_t* rows;
   int32_t* n;
+  Plan* plans;
   Token* token;
   uint16_t* xc;
 };
@@ -920,33 +1037,29 @@ Common take_common(Parts& w, int64_t T, int64_t D) {
   c.pos = w.take<int32_t>(T);
   c.rows = w.take<int32_t>(T);
   c.n = w.take<int32_t>(1);
+  c.plans = w.take<Plan>(kPlans);
   c.token = w.take<Token>(T);
   c.xc = w.take<uint16_t>(T * D);
   return c;
 }
 
+// Batches of so few tokens that there is little to leave out: the forward
+// takes them as they are, without the three passes before the product.
+constexpr int64_t kAsTheyAre = 256;
+
 struct Forward {
   Common c;
   float2* part;
   float* logit;
-  int32_t parts;
-  bool small;
+  double* lse64;
 };
 
-// Whether a product of np x nq outputs takes 256 x 128 tiles.
-bool small_tiles(int64_t np, int64_t nq, int64_t splits) {
-  const int64_t large = up(((np + 255) / 256) * ((nq + 255) / 256) * splits, 256) / 256;
-  const int64_t small = up(((np + 255) / 256) * ((nq + 127) / 128) * splits, 256) / 256;
-  return small * 10 < large * 18;
-}
-
 Forward take_forward(Parts& w, int64_t T, int64_t V, int64_t D) {
-  Forward f;
-  f.c = take_common(w, T, D);
-  f.small = small_tiles(V, T, 1);
-  f.parts = (int32_t)((V + 255) / 256 * (f.small ? Small::WP : Large::WP));
-  f.part = w.take<float2>(f.parts * T);
+  Forward f{};
+  if (T > kAsTheyAre) f.c = take_common(w, T, D);
+  f.part = w.take<float2>((V + 255) / 256 * Small::WP * T);
   f.logit = w.take<float>(T);
+  f.lse64 = w.take<double>(T);
   return f;
 }
 
@@ -962,9 +1075,6 @@ struct Backward {
   Common c;
   float* top;
   uint16_t* dz;
-  uint16_t* dzt;
-  uint16_t* xt;
-  uint16_t* wt;
   float* dx32;
   int32_t* entry;
   uint16_t* value;
@@ -972,26 +1082,22 @@ struct Backward {
   int32_t splits;
 };
 
-// Parts of the input gradient's reduction: enough for 256 tiles, of at least
-// 1024 steps each.
+// Most parts of the input gradient's reduction: of at least 1024 steps each,
+// 256 MiB in all.
 int32_t dx_splits(int64_t T, int64_t D, int64_t piece) {
-  const int64_t tiles = ((T + 255) / 256) * ((D + 127) / 128);
-  int64_t s = 256 / tiles;
+  int64_t s = (int64_t(1) << 26) / (up(T, 256) * D);
   if (s > piece / 1024) s = piece / 1024;
   return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
 Backward take_backward(Parts& w, int64_t T, int64_t V, int64_t D, int64_t k) {
-  Backward b;
+  Backward b{};
   b.c = take_common(w, T, D);
   b.rows_t = up(T, 256);
   b.piece = piece_of(T, V);
   b.splits = dx_splits(T, D, b.piece);
   b.top = w.take<float>(2);
   b.dz = w.take<uint16_t>(b.rows_t * b.piece);
-  b.dzt = w.take<uint16_t>(b.rows_t * b.piece);
-  b.xt = w.take<uint16_t>(b.rows_t * D);
-  b.wt = w.take<uint16_t>(b.piece * D);
   b.dx32 = w.take<float>(b.splits * b.rows_t * D);
   b.entry = w.take<int32_t>(T * k);
   b.value = w.take<uint16_t>(T * k);
@@ -1003,17 +1109,13 @@ unsigned blocks_for(int64_t items, int64_t per, int64_t most) {
   return (unsigned)(b < 1 ? 1 : b > most ? most : b);
 }
 
-template <int EPI, class C>
-int run_nt(const NtArgs& a, hipStream_t s) {
-  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&nt_kernel<EPI, C>),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-  if (set != hipSuccess) return set;
-  hipLaunchKernelGGL((nt_kernel<EPI, C>), dim3(256), dim3(512), C::LDS, s, a);
-  return hipGetLastError();
-}
 template <int EPI>
-int run_nt(const NtArgs& a, bool small, hipStream_t s) {
-  return small ? run_nt<EPI, Small>(a, s) : run_nt<EPI, Large>(a, s);
+int run_nt(const NtArgs& a, hipStream_t s) {
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&nt_kernel<EPI>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, Large::LDS);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL(nt_kernel<EPI>, dim3(256), dim3(512), Large::LDS, s, a);
+  return hipGetLastError();
 }
 
 #define MG_RUN(call)                       \
@@ -1023,11 +1125,12 @@ int run_nt(const NtArgs& a, bool small, hipStream_t s) {
   } while (0)
 
 // Which tokens count, their order and, packed, their rows of x.
-int place_tokens(const HeadArgs& a, const Common& c, float* top, hipStream_t s) {
+int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t splits, float* top, hipStream_t s) {
   const int64_t per = a.index != nullptr ? 4 : 256;
   hipLaunchKernelGGL(head_counts_kernel, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, s, a, c.pos);
   MG_RUN(hipGetLastError());
-  hipLaunchKernelGGL(head_place_kernel, dim3(1), dim3(1024), 0, s, a, c.pos, c.rows, c.n, c.token, top);
+  hipLaunchKernelGGL(head_place_kernel, dim3(1), dim3(1024), 0, s, a, c.pos, c.rows, c.n, c.token, c.plans,
+                     piece, splits, top);
   MG_RUN(hipGetLastError());
   hipLaunchKernelGGL(head_pack_kernel, dim3(blocks_for(a.T, 4, 2048)), dim3(256), 0, s, a.x, c.rows, c.n,
                      (int32_t)a.T, (int32_t)a.D, c.xc);
@@ -1041,13 +1144,14 @@ NtArgs logits_args(const HeadArgs& a, const Common& c, int64_t v0, int64_t count
   g.Q = {c.xc, (uint32_t)a.D * 2u, 128u};
   g.Q_all = a.x;
   g.n = c.n;
+  g.plan_at = c.plans != nullptr ? c.plans + kPlanLogits : nullptr;
   g.np = (int32_t)count;
   g.nq = g.tokens = (int32_t)a.T;
   g.K = g.D = (int32_t)a.D;
   g.first = (int32_t)v0;
+  g.target_first = a.first;
   g.gq = 8;
-  g.splits = 1;
-  g.scale = a.inv_temperature * kLog2e;
+  g.scale = a.scale;
   g.token = c.token;
   return g;
 }
@@ -1070,16 +1174,22 @@ int launch_head(const HeadArgs& a, hipStream_t s) {
   Parts w;
   w.base = static_cast<char*>(a.workspace);
   const Forward f = take_forward(w, a.T, a.V, a.D);
-  MG_RUN(place_tokens(a, f.c, nullptr, s));
+  if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, nullptr, s));
   NtArgs g = logits_args(a, f.c, 0, a.V);
+  g.plan = plan_of(a.V, a.T, a.D, 1, 0);
+  g.targets = f.c.pos != nullptr ? nullptr : a.targets;
   g.part = f.part;
   g.logit = a.index == nullptr ? f.logit : nullptr;
-  MG_RUN(run_nt<kStats>(g, f.small, s));
-  hipLaunchKernelGGL(head_join_kernel, dim3((unsigned)((a.T + 63) / 64)), dim3(1024), 0, s, a, f.c.pos,
-                     f.part, f.parts, f.logit);
+  MG_RUN(run_nt<kStats>(g, s));
+  if (a.T < 1024)
+    hipLaunchKernelGGL((head_join_kernel<1, 256>), dim3((unsigned)a.T), dim3(256), 0, s, a, f.c.pos, g.plan_at,
+                       g.plan, f.part, f.logit, f.lse64);
+  else
+    hipLaunchKernelGGL((head_join_kernel<16, 1024>), dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s, a,
+                       f.c.pos, g.plan_at, g.plan, f.part, f.logit, f.lse64);
   MG_RUN(hipGetLastError());
   if (a.index != nullptr) {
-    hipLaunchKernelGGL(head_entries_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(head_entries_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, f.lse64);
     MG_RUN(hipGetLastError());
   }
   return hipSuccess;
@@ -1096,69 +1206,56 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
   const Backward b = take_backward(w, a.T, a.V, a.D, a.index != nullptr ? a.k : 0);
   const int32_t T = (int32_t)a.T, D = (int32_t)a.D;
   const int64_t entries = a.index != nullptr ? a.T * a.k : 0;
-  MG_RUN(place_tokens(a, b.c, b.top, s));
+  MG_RUN(place_tokens(a, b.c, b.piece, b.splits, b.top, s));
   if (entries > 0) {
     hipLaunchKernelGGL(head_entry_values_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a,
                        b.c.pos, b.c.token, b.top, b.entry, b.value);
-    MG_RUN(hipGetLastError());
-  }
-  const unsigned cols = (unsigned)((D + 127) / 128);
-  if (a.dw != nullptr) {
-    hipLaunchKernelGGL(head_transpose_kernel, dim3((unsigned)((T + 63) / 64), cols), dim3(256), 0, s, a.x,
-                       b.c.rows, b.c.n, T, D, b.xt);
     MG_RUN(hipGetLastError());
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
     const int64_t count = a.V - v0 < b.piece ? a.V - v0 : b.piece;
     NtArgs g = logits_args(a, b.c, v0, count);
     g.top = b.top;
-    g.dz = a.dx != nullptr ? b.dz : nullptr;
-    g.dzt = a.dw != nullptr ? b.dzt : nullptr;
+    g.dz = b.dz;
     g.rows_t = b.rows_t;
-    g.rows_v = b.piece;
-    MG_RUN(run_nt<kDz>(g, small_tiles(count, T, 1), s));
+    MG_RUN(run_nt<kDz>(g, s));
     if (entries > 0) {
       hipLaunchKernelGGL(head_entry_store_kernel, dim3(blocks_for(entries, 256, 2048)), dim3(256), 0, s,
-                         b.c.pos, b.entry, b.value, entries, a.k, (int32_t)v0, (int32_t)count, b.rows_t,
-                         b.piece, g.dz, g.dzt);
+                         b.c.pos, b.entry, b.value, entries, a.k, (int32_t)v0, (int32_t)count, b.rows_t, b.dz);
       MG_RUN(hipGetLastError());
     }
+    const Operand dz = {b.dz, 128u, (uint32_t)(b.rows_t * 128)};
+    NtArgs h{};
+    h.P = dz;
+    h.n = b.c.n;
+    h.tokens = T;
+    h.nq = h.D = D;
+    h.gq = 8;
+    h.top = b.top;
+    h.rows_t = b.rows_t;
     if (a.dx != nullptr) {
-      hipLaunchKernelGGL(head_transpose_kernel, dim3((unsigned)((count + 63) / 64), cols), dim3(256), 0, s,
-                         a.w + v0 * a.D, nullptr, nullptr, (int32_t)count, D, b.wt);
-      MG_RUN(hipGetLastError());
-      NtArgs h{};
-      h.P = {b.dz, 128u, (uint32_t)(b.rows_t * 128)};
-      h.Q = {b.wt, 128u, (uint32_t)(a.D * 128)};
-      h.n = b.c.n;
-      h.np = h.tokens = T;
-      h.nq = h.D = D;
-      h.K = (int32_t)up(count, 8);
-      h.gq = 8;
-      h.splits = b.splits;
+      h.Q = {a.w + v0 * a.D, (uint32_t)D * 2u, 128u};
+      h.plan_at = b.c.plans + kPlanDx;
+      h.np = T;
+      h.K = (int32_t)count;
       h.add = v0 > 0;
       h.dx = b.dx32;
-      h.rows_t = b.rows_t;
-      MG_RUN(run_nt<kDx>(h, small_tiles(T, D, b.splits), s));
+      MG_RUN(run_nt<kDx>(h, s));
     }
     if (a.dw != nullptr) {
-      NtArgs h{};
-      h.P = {b.dzt, 128u, (uint32_t)(b.piece * 128)};
-      h.Q = {b.xt, 128u, (uint32_t)(a.D * 128)};
-      h.n = b.c.n;
+      h.Q = {b.c.xc, (uint32_t)D * 2u, 128u};
+      h.Q_all = a.x;
+      h.plan_at = b.c.plans + kPlanDw;
       h.np = (int32_t)count;
-      h.tokens = h.K = T;
-      h.nq = h.D = D;
-      h.gq = 8;
-      h.splits = 1;
-      h.top = b.top;
+      h.K = T;
       h.dw = a.dw + v0 * a.D;
-      MG_RUN(run_nt<kDw>(h, small_tiles(count, D, 1), s));
+      MG_RUN(run_nt<kDw>(h, s));
     }
   }
   if (a.dx != nullptr) {
+    const int64_t first = a.V < b.piece ? a.V : b.piece;
     hipLaunchKernelGGL(head_dx_kernel, dim3(blocks_for(a.T * (D / 8), 256, 4096)), dim3(256), 0, s, b.c.pos,
-                       b.dx32, b.splits, b.rows_t, a.T, D, b.top, a.dx);
+                       b.dx32, b.c.plans + kPlanDx, (int32_t)((first + 127) / 128), b.rows_t, a.T, D, b.top, a.dx);
     MG_RUN(hipGetLastError());
   }
   return hipSuccess;

@@ -151,7 +151,9 @@ struct HeadArgs {
   const void* teacher;        // [T, k] fp32 or bf16, distillation
   const int32_t* index;       // [T, k], or NULL: cross entropy
   int32_t k, teacher_bf16;
-  float inv_temperature;      // 1 for cross entropy
+  double c;                   // 1 / temperature (1 for cross entropy)
+  float scale;                // c log2(e), rounded, and ...
+  double unscale;             // ... c / scale
   float* loss;                // forward: [T]
   float* lse;                 // [T]
   float* logits;              // [T] or [T, k]

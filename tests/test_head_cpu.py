@@ -90,8 +90,11 @@ ALL = [_loss, _loss_bwd, _distill, _distill_bwd]
 def test_sizes(call):
     for bad in (dict(T=-1), dict(T=(1 << 22) + 1), dict(V=0), dict(V=-1), dict(V=1 << 31), dict(D=0), dict(D=12), dict(D=-8),
                 dict(D=(1 << 20) + 8), dict(first=-1), dict(first=(1 << 31) - 8), dict(T=1 << 22, V=1 << 20), dict(V=1 << 21, D=1 << 20),
-                dict(n=0), dict(n=1000)):
+                dict(n=0)):
         assert call(**bad) == SHAPE, bad
+    k = 3 if call in (_distill, _distill_bwd) else 0
+    need = L.mg_head_bwd_workspace(4, 9, 16, k) if call in (_loss_bwd, _distill_bwd) else L.mg_head_workspace(4, 9, 16)
+    assert call(n=need - 1) == SHAPE and call(n=need) in (OK, DEV, 5)
     for ok in (dict(T=0), dict(T=0, x=None, t=None, ws=None, n=0) if call is _loss else dict(T=0)):
         assert call(**ok) in (OK, DEV), ok                    # (a gradient of no tokens still writes zeros)
 
