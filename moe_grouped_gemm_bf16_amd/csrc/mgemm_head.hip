@@ -97,13 +97,13 @@ enum { kStats = 0, kDz = 1, kDx = 2, kDw = 3 };
 
 // How a product's tiles are cut, by the number of tokens that count.
 struct Plan {
-  int32_t small;        // 256 x 128 tiles, not 256 x 256
+  int32_t large;        // tiles along P of 256 x 256, the others of 256 x 128
   int32_t splits;       // parts of the reduction (input gradient)
 };
 
 struct NtArgs {
   Operand P, Q;
-  const void* Q_all;        // x itself, taken when all tokens count
+  const void* Q_all;        // what is taken for Q when all tokens count
   const int32_t* n;         // device: tokens that count, NULL: all
   const Plan* plan_at;      // device, NULL: `plan`
   Plan plan;
@@ -398,15 +398,16 @@ __device__ __forceinline__ Item item_of(int id, int tp, int tq, int gq) {
 // XCD has a contiguous range of tiles, gq of them along Q at a time, that
 // share operand rows in its L2.
 template <int EPI, class C>
-__device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const int n_tok, char* lds) {
+__device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const int tp0, const int tp_end,
+                                         const int most_splits, const int part0, char* lds) {
   constexpr bool kLogits = EPI == kStats || EPI == kDz;
   const int np = EPI == kDx ? n_tok : a.np;
   const int nq = kLogits ? n_tok : a.nq;
   const int K = EPI == kDw ? n_tok : a.K;
-  const int tp = (np + C::BP - 1) / C::BP, tq = (nq + C::BQ - 1) / C::BQ;
+  const int tp = tp_end - tp0, tq = (nq + C::BQ - 1) / C::BQ;      // tiles tp0 .. tp_end - 1 along P
   // pairs of stages; an empty reduction takes one of zeros
   const int pairs = max(1, (K + 127) >> 7);
-  const int splits = EPI == kDx ? min(plan.splits, pairs) : 1;
+  const int splits = EPI == kDx ? min(most_splits, pairs) : 1;
   const int total = tp * tq * splits, xcd = blockIdx.x & 7, wgs = gridDim.x >> 3;
   const int per = total >> 3, rem = total & 7;
   int id = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
@@ -428,7 +429,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const
   auto aim = [&](const Item& t, bool live) {
     int k0, m;
     range(t, k0, m);
-    c.source(a.P.base, Qp, live, t.ip * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
+    c.source(a.P.base, Qp, live, (tp0 + t.ip) * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
     return m;
   };
   Item t = item_of(id, tp, tq, a.gq), ahead = t;
@@ -456,10 +457,10 @@ __device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const
       c.pair();
       --left;
     }
-    const int pw = t.ip * C::BP + wp * 32 * C::MH, qw = t.iq * C::BQ + wq * 32;
+    const int p0 = (tp0 + t.ip) * C::BP, pw = p0 + wp * 32 * C::MH, qw = t.iq * C::BQ + wq * 32;
 
     if constexpr (EPI == kStats) {
-      if (t.ip * C::BP + C::BP > np) {
+      if (p0 + C::BP > np) {
         const int rows = np - pw - 4 * h;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
@@ -513,12 +514,12 @@ __device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const
           }
         s0 += s1;
         s0 += __shfl_xor(s0, 32);
-        if (h == 0 && q < nq) a.part[(int64_t)(t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
+        if (h == 0 && q < nq) a.part[(int64_t)(part0 + t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
       }
     }
 
     if constexpr (EPI == kDz) {
-      const bool edge_p = t.ip * C::BP + C::BP > np;
+      const bool edge_p = p0 + C::BP > np;
       const float inv = a.top[1];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -582,7 +583,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const
           }
         }
       };
-      const bool whole = t.ip * C::BP + C::BP <= np && t.iq * C::BQ + C::BQ <= nq;
+      const bool whole = p0 + C::BP <= np && t.iq * C::BQ + C::BQ <= nq;
       if (whole && a.add) store(std::true_type{}, std::true_type{});
       else if (whole) store(std::true_type{}, std::false_type{});
       else if (a.add) store(std::false_type{}, std::true_type{});
@@ -611,7 +612,15 @@ __device__ __forceinline__ void products(const NtArgs& a, const Plan plan, const
     if (id >= end) break;
     t = ahead;
   }
-  wait_vm<0>();       // the loads in flight write this workgroup's LDS
+  // the loads in flight write this workgroup's LDS, which its next tiles take
+  wait_vm<0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Parts of the forward's sums before tile ip along P.
+__host__ __device__ __forceinline__ int parts_before(int ip, int large) {
+  return ip < large ? ip * Large::WP : large * Large::WP + (ip - large) * Small::WP;
 }
 
 template <int EPI>
@@ -620,11 +629,12 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
   const int n = a.n != nullptr ? __builtin_amdgcn_readfirstlane(*a.n) : a.tokens;
   Plan plan = a.plan;
   if (a.plan_at != nullptr) {
-    plan.small = __builtin_amdgcn_readfirstlane(a.plan_at->small);
+    plan.large = __builtin_amdgcn_readfirstlane(a.plan_at->large);
     plan.splits = __builtin_amdgcn_readfirstlane(a.plan_at->splits);
   }
-  if (plan.small) products<EPI, Small>(a, plan, n, lds);
-  else products<EPI, Large>(a, plan, n, lds);
+  const int tp = ((EPI == kDx ? n : a.np) + 255) / 256, large = min(plan.large, tp);
+  products<EPI, Large>(a, n, 0, large, plan.splits, 0, lds);
+  products<EPI, Small>(a, n, large, tp, plan.splits, parts_before(large, large), lds);
 }
 
 // ------------------------------------------------------------ token passes --
@@ -682,14 +692,8 @@ __device__ __forceinline__ bool teacher_row(const HeadArgs& a, int64_t t, int la
   return true;
 }
 
-// Which tokens count (pos[t] = 0, else -1): one thread per token, or, for a
-// teacher's entries, one wave.
-__global__ __launch_bounds__(256) void head_counts_kernel(const HeadArgs a, int32_t* pos) {
-  if (a.index == nullptr) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t < a.T) pos[t] = a.targets[t] >= 0 ? 0 : -1;
-    return;
-  }
+// Which tokens have an entry of the teacher.  One wave per token.
+__global__ __launch_bounds__(256) void head_flags_kernel(const HeadArgs a, uint8_t* flag) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.T) return;
@@ -697,66 +701,94 @@ __global__ __launch_bounds__(256) void head_counts_kernel(const HeadArgs a, int3
   for (int j = lane; j < a.k; j += 64)
     any |= a.index[t * a.k + j] >= 0 && teacher_value(a, t * a.k + j) > -INFINITY;
   const bool counts = __builtin_amdgcn_ballot_w64(any) != 0;
-  if (lane == 0) pos[t] = counts ? 0 : -1;
+  if (lane == 0) flag[t] = counts;
 }
 
-// The time of a product's tiles, in ns: rounds of the chip's 256 compute units,
-// each of a tile's pairs of stages and its epilogue; for a split reduction the
-// parts' way through memory besides.  Measured: TIMES.
-__host__ __device__ __forceinline__ int64_t tile_time(bool small, int64_t np, int64_t nq, int64_t pairs,
-                                                      int64_t splits, int64_t out) {
-  const int64_t tiles = ((np + 255) / 256) * (small ? (nq + 127) / 128 : (nq + 255) / 256) * splits;
-  const int64_t rounds = (tiles + 255) / 256, each = (pairs + splits - 1) / splits;
-  return rounds * (small ? 1350 * each + 3000 : 2400 * each + 5000) + (splits > 1 ? splits * out / 640 : 0);
+// The products' plans.  Times in ns: a tile of 256 x 256 takes 2950 per pair of
+// stages (128 steps; 1390 TFLOP/s over 256 compute units), one of 256 x 128
+// 1900, and its epilogue `el`, `es` more; tiles run in rounds of the chip's 256
+// compute units.  (Measured on 2048 tokens, V = 65536, D = 1024 and 2048, each
+// size alone: forward 4200 and 100, dz 12000 and 7200, dw 9200 and 1100.)
+struct Cost {
+  int el, es;
+};
+__host__ __device__ __forceinline__ Cost cost_of(int epi) {
+  return epi == kStats ? Cost{4200, 300} : epi == kDz ? Cost{12000, 7000} : epi == kDw ? Cost{9000, 3000} : Cost{5000, 3000};
 }
+__host__ __device__ __forceinline__ int rounds_of(int tiles) { return (tiles + 255) >> 8; }
 
-// The quicker of the two tile sizes and of up to `most` parts.
-__host__ __device__ __forceinline__ Plan plan_of(int64_t np, int64_t nq, int64_t K, int most, int64_t out) {
-  const int64_t pairs = K > 128 ? (K + 127) / 128 : 1;
-  Plan best = {0, 1};
-  int64_t least = tile_time(false, np, nq, pairs, 1, out);
-  for (int i = 1; i < 24; ++i) {
-    // parts 1, 2, 3, 4, 6, 8, 12, .. 64
-    const int k = i >> 1, s = k < 2 ? k + 1 : (k & 1 ? 4 : 3) << (k - 2) / 2;
-    if (s > most) break;
-    const int64_t t = tile_time(i & 1, np, nq, pairs, s, out);
-    if (t < least) {
+// How many tiles along P are large: whole rounds of them, or all; what is left
+// over in small ones, where it would fill half a round or less.
+__host__ __device__ __forceinline__ Plan plan_of(int epi, int np, int nq, int K) {
+  const int tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
+  const int pairs = K > 128 ? (K + 127) / 128 : 1;
+  const Cost e = cost_of(epi);
+  const int64_t large = 2950 * (int64_t)pairs + e.el, small = 1900 * (int64_t)pairs + e.es;
+  const int full = (int)((int64_t)tp * tl / 256);
+  Plan best = {tp, 1};
+  int64_t least = -1;
+  for (int i = 0; i < 4; ++i) {
+    // all, none, all whole rounds, all but one of them
+    const int m = i == 0 ? tp : i == 1 || tl == 0 ? 0 : (int)((int64_t)(full - (i - 2)) * 256 / tl);
+    if (m < 0) continue;
+    const int64_t t = rounds_of(m * tl) * large + rounds_of((tp - m) * ts) * small + (m > 0 && m < tp ? 3000 : 0);
+    if (least < 0 || t < least) {
       least = t;
-      best.small = i & 1;
-      best.splits = s;
+      best.large = m;
     }
   }
   return best;
 }
 
-// Plans of a call's products.
+// The input gradient's tile size and parts, choice i of 24: parts 1, 2, 3, 4,
+// 6, 8, 12, .. 64, every part's way to memory and back at 6.4 values a ns.
+__host__ __device__ __forceinline__ Plan dx_choice(int i, int np, int nq, int K, int64_t* time) {
+  const int k = i >> 1, s = k < 2 ? k + 1 : (k & 1 ? 4 : 3) << (k - 2) / 2;
+  const int pairs = K > 128 ? (K + 127) / 128 : 1, tp = (np + 255) / 256;
+  const Cost e = cost_of(kDx);
+  const int each = (pairs + s - 1) / s;
+  const int tiles = tp * (i & 1 ? (nq + 127) / 128 : (nq + 255) / 256) * s;
+  *time = rounds_of(tiles) * (i & 1 ? 1900 * (int64_t)each + e.es : 2950 * (int64_t)each + e.el) +
+          (int64_t)s * np * nq / 640;
+  return Plan{i & 1 ? 0 : tp, s};
+}
+
 enum { kPlanLogits = 0, kPlanDx = 1, kPlanDw = 2, kPlans = 3 };
 
-// The counting tokens in order: pos[t] becomes a token's place (-1 for none),
-// rows[place] its token, n their number; per place what the epilogues need,
-// the products' plans and, backward, the largest weight.  One workgroup.
-__global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, int32_t* pos, int32_t* rows,
-                                                          int32_t* n, Token* token, Plan* plans, int64_t piece,
-                                                          int32_t splits, float* top) {
-  __shared__ int counts[16];
+// The counting tokens in order: pos[t] their place (-1 for the others),
+// rows[place] the token, n their number; per place what the epilogues need,
+// the products' plans and, backward, the largest weight.  The first workgroup
+// writes all that.  With `pack` every workgroup goes through the tokens, and
+// packs its share of the rows of x (stride `ld`; nothing where all tokens count
+// and x's own rows start on 128 bytes): for short batches, one launch for two.
+constexpr int kPlaceList = 64;         // rows of a workgroup's share
+__global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, const uint8_t* flag, int32_t* pos,
+                                                          int32_t* rows, int32_t* n, Token* token,
+                                                          Plan* plans, int32_t piece, int32_t splits,
+                                                          float* top, uint16_t* pack, int32_t ld) {
+  __shared__ int counts[2][16];
   __shared__ float tops[16];
+  __shared__ int list[kPlaceList];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int base = 0;
+  const bool head = blockIdx.x == 0;
+  int base = 0, turn = 0;
   float most = 0.f;
-  for (int64_t b = 0; b < a.T; b += 1024) {
+  for (int64_t b = 0; b < a.T; b += 1024, turn ^= 1) {
     const int64_t t = b + threadIdx.x;
-    const bool in = t < a.T && pos[t] >= 0;
+    const bool in = t < a.T && (a.index != nullptr ? flag[t] != 0 : a.targets[t] >= 0);
     const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
-    if (lane == 0) counts[wave] = __popcll(mask);
+    if (lane == 0) counts[turn][wave] = __popcll(mask);
     __syncthreads();
     int before = base + __popcll(mask & ((1ull << lane) - 1)), all = 0;
+#pragma unroll
     for (int w = 0; w < 16; ++w) {
-      const int v = counts[w];
+      const int v = counts[turn][w];
       if (w < wave) before += v;
       all += v;
     }
-    if (in) {
-      pos[t] = before;
+    if (in && pack != nullptr && before % gridDim.x == blockIdx.x) list[before / gridDim.x] = (int)t;
+    if (head && t < a.T) pos[t] = in ? before : -1;
+    if (head && in) {
       rows[before] = (int32_t)t;
       Token k = {0.f, 0.f, 0.f, -1};
       if (a.index == nullptr) {
@@ -772,35 +804,57 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, int3
       token[before] = k;
     }
     base += all;
-    __syncthreads();
   }
-  if (threadIdx.x == 0) *n = base;
-  // (a thread for each, on waves of their own)
-  if (threadIdx.x == 64) plans[kPlanLogits] = plan_of(piece, base, a.D, 1, 0);
-  if (top == nullptr) return;
-  if (threadIdx.x == 128) plans[kPlanDx] = plan_of(base, a.D, piece, splits, (int64_t)base * a.D);
-  if (threadIdx.x == 192) plans[kPlanDw] = plan_of(piece, a.D, base, 1, 0);
-  most = wave_max(most);
-  if (lane == 0) tops[wave] = most;
+  if (head) {
+    if (threadIdx.x == 0) *n = base;
+    if (threadIdx.x == 960) plans[kPlanLogits] = plan_of(top == nullptr ? kStats : kDz, piece, base, (int)a.D);
+    if (top != nullptr) {
+      if (threadIdx.x == 896) plans[kPlanDw] = plan_of(kDw, piece, (int)a.D, base);
+      if (wave == 13) {
+        int64_t time;
+        Plan p = dx_choice(lane < 24 ? lane : 0, base, (int)a.D, piece, &time);
+        if (p.splits > splits) time = INT64_MAX;
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+          const int64_t other = __shfl_xor(time, d);
+          const Plan q = {__shfl_xor(p.large, d), __shfl_xor(p.splits, d)};
+          if (other < time || (other == time && (q.splits < p.splits || (q.splits == p.splits && q.large > p.large)))) {
+            time = other;
+            p = q;
+          }
+        }
+        if (lane == 0) plans[kPlanDx] = p;
+      }
+      most = wave_max(most);
+      if (lane == 0) tops[wave] = most;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) most = fmaxf(most, tops[w]);
+        // a weight past the range where its inverse is a normal number is left as it is
+        const bool fit = most > 1e-37f && most < 1e37f;
+        top[0] = fit ? most : 1.f;
+        top[1] = fit ? 1.f / most : 1.f;
+      }
+    }
+  }
+  if (pack == nullptr || (base == a.T && ld == a.D)) return;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 16; ++w) most = fmaxf(most, tops[w]);
-    // a weight past the range where its inverse is a normal number is left as it is
-    const bool fit = most > 1e-37f && most < 1e37f;
-    top[0] = fit ? most : 1.f;
-    top[1] = fit ? 1.f / most : 1.f;
+  for (int i = wave; i * (int64_t)gridDim.x + blockIdx.x < base; i += 16) {
+    const u32x4* from = reinterpret_cast<const u32x4*>(a.x + (int64_t)list[i] * a.D);
+    u32x4* to = reinterpret_cast<u32x4*>(pack + ((int64_t)i * gridDim.x + blockIdx.x) * ld);
+    for (int c = lane; c < a.D / 8; c += 64) to[c] = from[c];
   }
 }
 
-// xc[place] = x[rows[place]], unless all tokens count.  One wave per row.
+// xc[place] = x[rows[place]], as the kernel above.  One wave per row.
 __global__ __launch_bounds__(256) void head_pack_kernel(const uint16_t* x, const int32_t* rows,
                                                         const int32_t* n, int32_t T, int32_t D,
-                                                        uint16_t* xc) {
+                                                        uint16_t* xc, int32_t ld) {
   const int count = *n;
-  if (count == T) return;
+  if (count == T && ld == D) return;
   for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < count; p += (int64_t)gridDim.x * 4) {
     const u32x4* from = reinterpret_cast<const u32x4*>(x + (int64_t)rows[p] * D);
-    u32x4* to = reinterpret_cast<u32x4*>(xc + p * D);
+    u32x4* to = reinterpret_cast<u32x4*>(xc + p * ld);
     for (int i = threadIdx.x & 63; i < D / 8; i += 64) to[i] = from[i];
   }
 }
@@ -816,8 +870,7 @@ __global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const i
   __shared__ float2 got[NT / 64][TT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = threadIdx.x % TT;
   const int64_t t = (int64_t)blockIdx.x * TT + tok;
-  const int small = plan_at != nullptr ? plan_at->small : plan.small;
-  const int parts = (int)((a.V + 255) / 256) * (small ? Small::WP : Large::WP);
+  const int parts = parts_before((int)((a.V + 255) / 256), plan_at != nullptr ? plan_at->large : plan.large);
   int p = -1;
   if (t < a.T) p = pos != nullptr ? pos[t] : a.index != nullptr || a.targets[t] >= 0 ? (int)t : -1;
   float top = -INFINITY, sum = 0.f;
@@ -989,6 +1042,7 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const int32_t* pos, const 
     u32x4 v = {0, 0, 0, 0};
     if (p >= 0) {
       float s[8] = {};
+#pragma unroll 4
       for (int k = 0; k < splits; ++k) {
         const float4* f = reinterpret_cast<const float4*>(dx32 + (k * rows_t + p) * D + d);
         const float4 lo = f[0], hi = f[1];
@@ -1025,6 +1079,7 @@ struct Parts {
 };
 
 struct Common {
+  uint8_t* flag;
   int32_t* pos;
   int32_t* rows;
   int32_t* n;
@@ -1034,12 +1089,13 @@ struct Common {
 };
 Common take_common(Parts& w, int64_t T, int64_t D) {
   Common c;
+  c.flag = w.take<uint8_t>(T);
   c.pos = w.take<int32_t>(T);
   c.rows = w.take<int32_t>(T);
   c.n = w.take<int32_t>(1);
   c.plans = w.take<Plan>(kPlans);
   c.token = w.take<Token>(T);
-  c.xc = w.take<uint16_t>(T * D);
+  c.xc = w.take<uint16_t>(T * up(D, 64));
   return c;
 }
 
@@ -1126,14 +1182,19 @@ int run_nt(const NtArgs& a, hipStream_t s) {
 
 // Which tokens count, their order and, packed, their rows of x.
 int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t splits, float* top, hipStream_t s) {
-  const int64_t per = a.index != nullptr ? 4 : 256;
-  hipLaunchKernelGGL(head_counts_kernel, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, s, a, c.pos);
+  if (a.index != nullptr) {
+    hipLaunchKernelGGL(head_flags_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, c.flag);
+    MG_RUN(hipGetLastError());
+  }
+  const int32_t ld = (int32_t)up(a.D, 64);
+  const bool both = a.T <= 256 * kPlaceList;
+  hipLaunchKernelGGL(head_place_kernel, dim3(both ? blocks_for(a.T, 16, 256) : 1), dim3(1024), 0, s, a, c.flag,
+                     c.pos, c.rows, c.n, c.token, c.plans, (int32_t)piece, splits, top,
+                     both ? c.xc : nullptr, ld);
   MG_RUN(hipGetLastError());
-  hipLaunchKernelGGL(head_place_kernel, dim3(1), dim3(1024), 0, s, a, c.pos, c.rows, c.n, c.token, c.plans,
-                     piece, splits, top);
-  MG_RUN(hipGetLastError());
+  if (both) return hipSuccess;
   hipLaunchKernelGGL(head_pack_kernel, dim3(blocks_for(a.T, 4, 2048)), dim3(256), 0, s, a.x, c.rows, c.n,
-                     (int32_t)a.T, (int32_t)a.D, c.xc);
+                     (int32_t)a.T, (int32_t)a.D, c.xc, ld);
   return hipGetLastError();
 }
 
@@ -1141,8 +1202,11 @@ int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t spli
 NtArgs logits_args(const HeadArgs& a, const Common& c, int64_t v0, int64_t count) {
   NtArgs g{};
   g.P = {a.w + v0 * a.D, (uint32_t)a.D * 2u, 128u};
-  g.Q = {c.xc, (uint32_t)a.D * 2u, 128u};
-  g.Q_all = a.x;
+  // x's rows packed, or as they are where all count and every row starts on 128
+  // bytes: a staged row that crosses a line is two reads of L2 each time
+  const bool packed = c.xc != nullptr;
+  g.Q = {c.xc, (uint32_t)(packed ? up(a.D, 64) : a.D) * 2u, 128u};
+  g.Q_all = packed && a.D % 64 != 0 ? c.xc : a.x;
   g.n = c.n;
   g.plan_at = c.plans != nullptr ? c.plans + kPlanLogits : nullptr;
   g.np = (int32_t)count;
@@ -1176,7 +1240,7 @@ int launch_head(const HeadArgs& a, hipStream_t s) {
   const Forward f = take_forward(w, a.T, a.V, a.D);
   if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, nullptr, s));
   NtArgs g = logits_args(a, f.c, 0, a.V);
-  g.plan = plan_of(a.V, a.T, a.D, 1, 0);
+  g.plan = plan_of(kStats, (int)a.V, (int)a.T, (int)a.D);
   g.targets = f.c.pos != nullptr ? nullptr : a.targets;
   g.part = f.part;
   g.logit = a.index == nullptr ? f.logit : nullptr;
@@ -1243,8 +1307,8 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
       MG_RUN(run_nt<kDx>(h, s));
     }
     if (a.dw != nullptr) {
-      h.Q = {b.c.xc, (uint32_t)D * 2u, 128u};
-      h.Q_all = a.x;
+      h.Q = g.Q;
+      h.Q_all = g.Q_all;
       h.plan_at = b.c.plans + kPlanDw;
       h.np = (int32_t)count;
       h.K = T;

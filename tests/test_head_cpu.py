@@ -131,7 +131,8 @@ def test_workspace_sizes():
     assert L.mg_head_bwd_workspace(4, 9, 16, 257) == 0 and L.mg_head_bwd_workspace(4, 9, 16, -1) == 0
     for T, V, D in ((1, 1, 8), (8192, 131072, 4096), (65536, 200000, 2048), (300, 100, 72)):
         fwd, bwd = L.mg_head_workspace(T, V, D), L.mg_head_bwd_workspace(T, V, D, 0)
-        assert 0 < fwd < 2 * T * D + 40 * T + 16 * T * (V / 128 + 4) + 4096
+        wide = -(-D // 64) * 64                       # packed rows of x start on 128 bytes
+        assert 0 < fwd < 2 * T * wide + 40 * T + 16 * T * (V / 128 + 4) + 4096
         assert 0 < bwd < (1 << 31) + 12 * (T + 256) * D * 64 + (1 << 28) * 2 * D
         assert L.mg_head_bwd_workspace(T, V, D, 64) >= bwd + 6 * 64 * T
 
