@@ -704,16 +704,16 @@ __global__ __launch_bounds__(256) void head_flags_kernel(const HeadArgs a, uint8
   if (lane == 0) flag[t] = counts;
 }
 
-// The products' plans.  Times in ns: a tile of 256 x 256 takes 2950 per pair of
-// stages (128 steps; 1390 TFLOP/s over 256 compute units), one of 256 x 128
-// 1900, and its epilogue `el`, `es` more; tiles run in rounds of the chip's 256
-// compute units.  (Measured on 2048 tokens, V = 65536, D = 1024 and 2048, each
-// size alone: forward 4200 and 100, dz 12000 and 7200, dw 9200 and 1100.)
+// The products' plans.  Times in ns: a tile of 256 x 256 takes 3100 per pair of
+// stages (128 steps), one of 256 x 128 1850, and its epilogue `el`, `es` more;
+// tiles run in rounds of the chip's 256 compute units.  (Measured on 2048
+// tokens, V = 65536, D = 512 to 2048, either size alone.  The epilogues that
+// write are the burst of all units' stores: 34 MB of dz in 8 us.)
 struct Cost {
   int el, es;
 };
 __host__ __device__ __forceinline__ Cost cost_of(int epi) {
-  return epi == kStats ? Cost{4200, 300} : epi == kDz ? Cost{12000, 7000} : epi == kDw ? Cost{9000, 3000} : Cost{5000, 3000};
+  return epi == kStats ? Cost{3900, 1700} : epi == kDz ? Cost{12000, 6000} : epi == kDw ? Cost{11000, 5000} : Cost{5000, 3000};
 }
 __host__ __device__ __forceinline__ int rounds_of(int tiles) { return (tiles + 255) >> 8; }
 
@@ -723,7 +723,7 @@ __host__ __device__ __forceinline__ Plan plan_of(int epi, int np, int nq, int K)
   const int tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
   const int pairs = K > 128 ? (K + 127) / 128 : 1;
   const Cost e = cost_of(epi);
-  const int64_t large = 2950 * (int64_t)pairs + e.el, small = 1900 * (int64_t)pairs + e.es;
+  const int64_t large = 3100 * (int64_t)pairs + e.el, small = 1850 * (int64_t)pairs + e.es;
   const int full = (int)((int64_t)tp * tl / 256);
   Plan best = {tp, 1};
   int64_t least = -1;
@@ -748,7 +748,7 @@ __host__ __device__ __forceinline__ Plan dx_choice(int i, int np, int nq, int K,
   const Cost e = cost_of(kDx);
   const int each = (pairs + s - 1) / s;
   const int tiles = tp * (i & 1 ? (nq + 127) / 128 : (nq + 255) / 256) * s;
-  *time = rounds_of(tiles) * (i & 1 ? 1900 * (int64_t)each + e.es : 2950 * (int64_t)each + e.el) +
+  *time = rounds_of(tiles) * (i & 1 ? 1850 * (int64_t)each + e.es : 3100 * (int64_t)each + e.el) +
           (int64_t)s * np * nq / 640;
   return Plan{i & 1 ? 0 : tp, s};
 }
