@@ -12,7 +12,7 @@
 // C[q, p] = sum_r Q[q, r] P[p, r]:
 //   logits (forward, backward)  P = w rows, Q = x rows, r = hidden column
 //   input gradient              P = dz rows (tokens), Q = w columns, r = vocabulary
-//   weight gradient             P = dz columns (vocabulary), Q = x columns, r = token
+//   weight gradient             P = x columns, Q = dz columns (vocabulary), r = token
 // The forward's epilogue turns a tile of logits into one (maximum, sum of
 // exponentials) per token and 64 or 128 vocabulary entries; the backward's turns
 // it into dz, in 16 bits, for a piece of the vocabulary at a time.  dz lies in
@@ -103,7 +103,7 @@ struct Plan {
 
 struct NtArgs {
   Operand P, Q;
-  const void* Q_all;        // what is taken for Q when all tokens count
+  const void* x_all;        // what is taken for x when all tokens count
   const int32_t* n;         // device: tokens that count, NULL: all
   const Plan* plan_at;      // device, NULL: `plan`
   Plan plan;
@@ -361,20 +361,47 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// 4 x 4 transpose over the four lanes of a quad: lane i brings column i of
-// four rows as (row 0, row 1), (row 2, row 3) and gets row i of four columns.
-__device__ __forceinline__ u32x2 quad_transpose(uint32_t lo, uint32_t hi, int lane) {
-  const bool up = lane & 2;
-  const uint32_t send = up ? lo : hi, own = up ? hi : lo;
-  const uint32_t recv = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0x4E, 0xF, 0xF, true);  // lane ^ 2
-  const uint32_t x = up ? recv : own, y = up ? own : recv;   // columns (i & 1), (i & 1) + 2
-  const uint32_t rx = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true);       // lane ^ 1
-  const uint32_t ry = (uint32_t)__builtin_amdgcn_mov_dpp((int)y, 0xB1, 0xF, 0xF, true);
-  const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;   // r's bytes are 4-7
-  u32x2 v;
-  v.x = __builtin_amdgcn_perm(rx, x, sel);
-  v.y = __builtin_amdgcn_perm(ry, y, sel);
-  return v;
+// Two blocks of 32 x 32 results, 16 bits each, lane l holding of row l % 32
+// columns 8 g + 4 (l / 32) .. + 3 in x[2 g], x[2 g + 1], to 16 bytes of one row:
+// out[e] is of row (l % 32 & ~3) + e columns 8 (l % 4) .. + 7, of block a in
+// lanes 0-31 and of block b in lanes 32-63.  So a store writes 64 contiguous
+// bytes per row and block, where the registers as they are would give 16: the
+// stores' requests, not their bytes, are what an epilogue waits for (dz of 8192
+// x 131072, D = 4096: 7.0 -> 6.8 ms; dw of 96 tokens, V = 32768,
+// D = 2048: 48 -> 35 us).
+__device__ __forceinline__ void regroup(const uint32_t (&a)[8], const uint32_t (&b)[8], u32x4 (&out)[4],
+                                        int lane) {
+  uint32_t r[4][4];                  // [column group][dword]: the row's 16 bytes
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      // the upper half of a's register for the lower half of b's
+      const auto v = __builtin_amdgcn_permlane32_swap(a[2 * g + d], b[2 * g + d], false, false);
+      r[g][d] = v[0];
+      r[g][2 + d] = v[1];
+    }
+  // 4 x 4 transposes over the four lanes of a quad: with the neighbour, then
+  // with the lane two on
+  const bool odd = lane & 1, up = lane & 2;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t t[4];
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      const uint32_t x = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[g][d], 0xB1, 0xF, 0xF, true);
+      const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[g + 1][d], 0xB1, 0xF, 0xF, true);
+      t[g] = odd ? y : r[g][d];
+      t[g + 1] = odd ? r[g + 1][d] : x;
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t x = (uint32_t)__builtin_amdgcn_mov_dpp((int)t[g], 0x4E, 0xF, 0xF, true);
+      const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)t[g + 2], 0x4E, 0xF, 0xF, true);
+      out[g][d] = up ? y : t[g];
+      out[g + 2][d] = up ? t[g + 2] : x;
+    }
+  }
 }
 
 // A work item: tile (ip, iq) and, input gradient, part of the reduction.
@@ -413,7 +440,10 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   int id = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
   const int end = xcd * per + min(xcd, rem) + per + (xcd < rem ? 1 : 0);
   if (id >= end) return;
-  const void* Qp = EPI != kDx && n_tok == a.tokens ? a.Q_all : a.Q.base;
+  // x, as it is where all tokens count
+  const bool all = n_tok == a.tokens;
+  const void* Pp = EPI == kDw && all ? a.x_all : a.P.base;
+  const void* Qp = kLogits && all ? a.x_all : a.Q.base;
 
   Core<C, EPI == kDw, !kLogits> c;
   c.init(a, lds);
@@ -429,7 +459,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   auto aim = [&](const Item& t, bool live) {
     int k0, m;
     range(t, k0, m);
-    c.source(a.P.base, Qp, live, (tp0 + t.ip) * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
+    c.source(Pp, Qp, live, (tp0 + t.ip) * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
     return m;
   };
   Item t = item_of(id, tp, tq, a.gq), ahead = t;
@@ -529,30 +559,40 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
         const float wa = tk.a * inv, wb = tk.b * inv;
         const int rel = tk.target < 0 ? -1 : tk.target - a.first - pw;
         const bool told = __builtin_amdgcn_ballot_w64(rel >= 0 && rel < C::BP) != 0;
-        char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)(pw >> 6) * a.rows_t + q) * 128 + 2 * (pw & 63) + 8 * h;
+        // block i of the lane's half after the regrouping, its four rows of dz
+        const int pb = pw + (lane < 32 ? 0 : p_row(1)), q4 = qw + C::BQ / 2 * j + (l32 & ~3);
+        char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)(pb >> 6) * a.rows_t + q4) * 128 +
+                   2 * (pb & 63) + 16 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < MP; ++i) {
-          f32x16 v;
+        for (int i = 0; i < MP; i += 2) {
+          uint32_t pk[2][8];
 #pragma unroll
-          for (int g = 0; g < 16; ++g)
-            v[g] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][g], a.scale, -tk.lse2));
-          if (told) {
-#pragma unroll
-            for (int g = 0; g < 16; ++g) v[g] -= rel - 4 * h == p_row(i) + 8 * (g >> 2) + (g & 3) ? wb : 0.f;
-          }
-          if (edge_p) {
+          for (int u = 0; u < 2; ++u) {
+            f32x16 v;
 #pragma unroll
             for (int g = 0; g < 16; ++g)
-              v[g] = p_row(i) + 8 * (g >> 2) + (g & 3) < np - pw - 4 * h ? v[g] : 0.f;
-          }
-          if (i == C::MH) dz += C::BP / 128 * a.rows_t * 128;
+              v[g] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i + u][j][g], a.scale, -tk.lse2));
+            if (told) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+              for (int g = 0; g < 16; ++g)
+                v[g] -= rel - 4 * h == p_row(i + u) + 8 * (g >> 2) + (g & 3) ? wb : 0.f;
+            }
+            if (edge_p) {
+#pragma unroll
+              for (int g = 0; g < 16; ++g)
+                v[g] = p_row(i + u) + 8 * (g >> 2) + (g & 3) < np - pw - 4 * h ? v[g] : 0.f;
+            }
             // the one rounding of dz: a 16-bit operand of the two products
-            *reinterpret_cast<u32x2*>(dz + 64 * (i % C::MH) + 16 * g) =
-                u32x2{pack2(v[4 * g], v[4 * g + 1]), pack2(v[4 * g + 2], v[4 * g + 3])};
+#pragma unroll
+            for (int g = 0; g < 8; ++g) pk[u][g] = pack2(v[2 * g], v[2 * g + 1]);
+            __builtin_amdgcn_sched_barrier(0);    // a block's values at a time: registers
           }
-          __builtin_amdgcn_sched_barrier(0);      // a block's values at a time: registers
+          u32x4 out[4];
+          regroup(pk[0], pk[1], out, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x4*>(dz + 128 * e) = out[e];
+          dz += C::BP / 128 * a.rows_t * 128;     // (Large) the other half's blocks
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
@@ -591,20 +631,28 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
     }
 
     if constexpr (EPI == kDw) {
+      // P = hidden columns, Q = vocabulary entries
       const float scale = a.top[0];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int d = qw + C::BQ / 2 * j + (l32 & ~3);
+        const int q4 = qw + C::BQ / 2 * j + (l32 & ~3);
 #pragma unroll
-        for (int i = 0; i < MP; ++i)
+        for (int i = 0; i < MP; i += 2) {
+          uint32_t pk[2][8];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const u32x2 v = quad_transpose(
-                pack2(c.acc[i][j][4 * g] * scale, c.acc[i][j][4 * g + 1] * scale),
-                pack2(c.acc[i][j][4 * g + 2] * scale, c.acc[i][j][4 * g + 3] * scale), lane);
-            const int p = pw + p_row(i) + 8 * g + 4 * h + (lane & 3);
-            if (p < np && d < nq) *reinterpret_cast<u32x2*>(a.dw + (int64_t)p * a.D + d) = v;
-          }
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              pk[u][g] = pack2(c.acc[i + u][j][2 * g] * scale, c.acc[i + u][j][2 * g + 1] * scale);
+          u32x4 out[4];
+          regroup(pk[0], pk[1], out, lane);
+          const int d = pw + (lane < 32 ? p_row(i) : p_row(i + 1)) + 8 * (lane & 3);
+          uint16_t* to = a.dw + (int64_t)q4 * a.D + d;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (q4 + e < nq && d < np) *reinterpret_cast<u32x4*>(to + (int64_t)e * a.D) = out[e];
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
 
@@ -809,7 +857,7 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
     if (threadIdx.x == 0) *n = base;
     if (threadIdx.x == 960) plans[kPlanLogits] = plan_of(top == nullptr ? kStats : kDz, piece, base, (int)a.D);
     if (top != nullptr) {
-      if (threadIdx.x == 896) plans[kPlanDw] = plan_of(kDw, piece, (int)a.D, base);
+      if (threadIdx.x == 896) plans[kPlanDw] = plan_of(kDw, (int)a.D, piece, base);
       if (wave == 13) {
         int64_t time;
         Plan p = dx_choice(lane < 24 ? lane : 0, base, (int)a.D, piece, &time);
@@ -1206,7 +1254,7 @@ NtArgs logits_args(const HeadArgs& a, const Common& c, int64_t v0, int64_t count
   // bytes: a staged row that crosses a line is two reads of L2 each time
   const bool packed = c.xc != nullptr;
   g.Q = {c.xc, (uint32_t)(packed ? up(a.D, 64) : a.D) * 2u, 128u};
-  g.Q_all = packed && a.D % 64 != 0 ? c.xc : a.x;
+  g.x_all = packed && a.D % 64 != 0 ? c.xc : a.x;
   g.n = c.n;
   g.plan_at = c.plans != nullptr ? c.plans + kPlanLogits : nullptr;
   g.np = (int32_t)count;
@@ -1290,27 +1338,30 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     }
     const Operand dz = {b.dz, 128u, (uint32_t)(b.rows_t * 128)};
     NtArgs h{};
-    h.P = dz;
     h.n = b.c.n;
     h.tokens = T;
-    h.nq = h.D = D;
+    h.D = D;
     h.gq = 8;
     h.top = b.top;
     h.rows_t = b.rows_t;
     if (a.dx != nullptr) {
+      h.P = dz;
       h.Q = {a.w + v0 * a.D, (uint32_t)D * 2u, 128u};
       h.plan_at = b.c.plans + kPlanDx;
       h.np = T;
+      h.nq = D;
       h.K = (int32_t)count;
       h.add = v0 > 0;
       h.dx = b.dx32;
       MG_RUN(run_nt<kDx>(h, s));
     }
     if (a.dw != nullptr) {
-      h.Q = g.Q;
-      h.Q_all = g.Q_all;
+      h.P = g.Q;
+      h.x_all = g.x_all;
+      h.Q = dz;
       h.plan_at = b.c.plans + kPlanDw;
-      h.np = (int32_t)count;
+      h.np = D;
+      h.nq = (int32_t)count;
       h.K = T;
       h.dw = a.dw + v0 * a.D;
       MG_RUN(run_nt<kDw>(h, s));
