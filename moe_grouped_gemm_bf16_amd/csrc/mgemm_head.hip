@@ -1341,7 +1341,7 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     h.n = b.c.n;
     h.tokens = T;
     h.D = D;
-    h.gq = 8;
+    h.gq = 4;
     h.top = b.top;
     h.rows_t = b.rows_t;
     if (a.dx != nullptr) {
