@@ -124,6 +124,7 @@ struct NtArgs {
   int64_t rows_t;           // T'
   float* dx;                // [splits][T'][D] fp32
   uint16_t* dw;             // [V, D]
+  float* dw_parts;          // [splits][V][D] fp32
   int32_t D;
 };
 
@@ -427,6 +428,7 @@ __device__ __forceinline__ Item item_of(int id, int tp, int tq, int gq) {
 template <int EPI, class C>
 __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const int tp0, const int tp_end,
                                          const int most_splits, const int part0, char* lds) {
+  constexpr bool kSplit = EPI == kDx || EPI == kDw;
   constexpr bool kLogits = EPI == kStats || EPI == kDz;
   const int np = EPI == kDx ? n_tok : a.np;
   const int nq = kLogits ? n_tok : a.nq;
@@ -434,10 +436,13 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   const int tp = tp_end - tp0, tq = (nq + C::BQ - 1) / C::BQ;      // tiles tp0 .. tp_end - 1 along P
   // pairs of stages; an empty reduction takes one of zeros
   const int pairs = max(1, (K + 127) >> 7);
-  const int splits = EPI == kDx ? min(most_splits, pairs) : 1;
+  const int splits = kSplit ? min(most_splits, pairs) : 1;
   const int total = tp * tq * splits, xcd = blockIdx.x & 7, wgs = gridDim.x >> 3;
   const int per = total >> 3, rem = total & 7;
-  int id = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
+  // (the weight gradient's list begins at the other end of an XCD's workgroups:
+  // the input gradient's has left those with the least)
+  const int wg = blockIdx.x >> 3;
+  int id = xcd * per + min(xcd, rem) + (EPI == kDw ? wgs - 1 - wg : wg);
   const int end = xcd * per + min(xcd, rem) + per + (xcd < rem ? 1 : 0);
   if (id >= end) return;
   // x, as it is where all tokens count
@@ -450,7 +455,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   auto range = [&](const Item& t, int& k0, int& m) {     // pairs [k0, k0 + m) of the item
     k0 = 0;
     m = pairs;
-    if (EPI == kDx) {
+    if (kSplit) {
       const int each = pairs / splits, more = pairs - each * splits;
       k0 = t.s * each + min(t.s, more);
       m = each + (t.s < more ? 1 : 0);
@@ -633,6 +638,20 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
     if constexpr (EPI == kDw) {
       // P = hidden columns, Q = vocabulary entries
       const float scale = a.top[0];
+      if (splits > 1) {          // parts in fp32, joined by head_sum_kernel
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int q = qw + C::BQ / 2 * j + l32;
+          float* to = a.dw_parts + ((int64_t)t.s * nq + q) * a.D + pw + 4 * h;
+#pragma unroll
+          for (int i = 0; i < MP; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (q < nq && pw + p_row(i) + 8 * g < np)
+                *reinterpret_cast<float4*>(to + p_row(i) + 8 * g) =
+                    make_float4(c.acc[i][j][4 * g], c.acc[i][j][4 * g + 1], c.acc[i][j][4 * g + 2], c.acc[i][j][4 * g + 3]);
+        }
+      } else
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int q4 = qw + C::BQ / 2 * j + (l32 & ~3);
@@ -672,8 +691,7 @@ __host__ __device__ __forceinline__ int parts_before(int ip, int large) {
 }
 
 template <int EPI>
-__global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
-  extern __shared__ char lds[];
+__device__ __forceinline__ void product(const NtArgs& a, char* lds) {
   const int n = a.n != nullptr ? __builtin_amdgcn_readfirstlane(*a.n) : a.tokens;
   Plan plan = a.plan;
   if (a.plan_at != nullptr) {
@@ -683,6 +701,165 @@ __global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
   const int tp = ((EPI == kDx ? n : a.np) + 255) / 256, large = min(plan.large, tp);
   products<EPI, Large>(a, n, 0, large, plan.splits, 0, lds);
   products<EPI, Small>(a, n, large, tp, plan.splits, parts_before(large, large), lds);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void nt_kernel(const NtArgs a) {
+  extern __shared__ char lds[];
+  product<EPI>(a, lds);
+}
+
+// Both gradients of a piece: a workgroup whose part of dx is done goes on with
+// dw, so that neither waits for the other's last tiles.
+__global__ __launch_bounds__(512, 2) void grads_kernel(const NtArgs x, const NtArgs w) {
+  extern __shared__ char lds[];
+  if (x.dx != nullptr) product<kDx>(x, lds);
+  if (w.dw != nullptr) product<kDw>(w, lds);
+}
+
+// The logits' product of small problems, on tiles of 64 x 64 whose reduction is
+// shared by the workgroup's eight waves, 64 steps in turn: where 256 x 128 tiles
+// would be fewer than the compute units, four to eight times as many
+// workgroups, each with an eighth of the steps (V = 700, 256 tokens, D = 4096:
+// the forward 53 -> 20 us).  A wave stages its own 64 x 64 parts of both operands
+// (16 KiB), takes them to registers, sends for the next and multiplies: no wave
+// waits for another until their sums meet in LDS, in a fixed order.
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
+  extern __shared__ char lds[];
+  float4* red = reinterpret_cast<float4*>(lds);          // [8 waves][16][64 lanes]
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nq = a.n != nullptr ? __builtin_amdgcn_readfirstlane(*a.n) : a.tokens, np = a.np, K = a.K;
+  const int p0 = blockIdx.x * 64, q0 = blockIdx.y * 64;
+  if (q0 >= nq) return;
+  if (p0 >= np) {                                        // (parts are counted in tiles of 256)
+    if (EPI == kStats && threadIdx.x < 64 && q0 + threadIdx.x < nq)
+      a.part[(int64_t)blockIdx.x * a.tokens + q0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const char* Q = static_cast<const char*>(nq == a.tokens ? a.x_all : a.Q.base);
+  // rows past the end repeat the last one, steps past it are zeros
+  const uint32_t mine = (uint32_t)(uintptr_t)(lds_char*)lds + (uint32_t)wave * 16384u;
+  const uint32_t r8 = lane >> 3, chunk = 16u * ((lane & 7) ^ r8);
+  const uint32_t most[2] = {(uint32_t)(min(64, np - p0) - 1) * a.P.stride, (uint32_t)(min(64, nq - q0) - 1) * a.Q.stride};
+  const uint32_t stride[2] = {a.P.stride, a.Q.stride};
+  const uint64_t base[2] = {reinterpret_cast<uint64_t>(a.P.base) + (uint64_t)p0 * a.P.stride,
+                            reinterpret_cast<uint64_t>(Q) + (uint64_t)q0 * a.Q.stride};
+  auto load = [&](int block) {
+    const uint32_t past = (int)(chunk >> 1) + 64 * block < K ? 0u : kOOB;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const i32x4 rsrc = make_rsrc(reinterpret_cast<const void*>(base[o] + 128 * (uint64_t)block), 0x7fffffffu);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        dma16(rsrc, mine + 8192u * o + 1024u * r, (min((r8 + 8 * r) * stride[o], most[o]) + chunk) | past);
+    }
+  };
+  f32x16 acc[2][2] = {};
+  const int blocks = (K + 63) / 64;
+  if (wave < blocks) load(wave);
+  for (int b = wave; b < blocks; b += 8) {
+    bf16x8 f[4][4];                                      // w, w, x, x
+    wait_vm<0>();
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i][kk] = *(lds_frag*)(uintptr_t)(mine + 4096u * i + 128u * l32 + (uint32_t)(((2 * kk + h) ^ (l32 & 7)) << 4));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (b + 8 < blocks) load(b + 8);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i][kk], f[2 + j][kk], acc[i][j], 0, 0, 0);
+  }
+  __syncthreads();                                       // the sums take the staged data's place
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        red[(wave * 16 + (2 * i + j) * 4 + g) * 64 + lane] =
+            make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+  __syncthreads();
+  // the wave's share: rows 32 i + 16 (wave & 1) + 8 g + 4 h + e, g < 2, of token q
+  const int i = wave >> 2, j = (wave >> 1) & 1, pw = p0 + 32 * i + 16 * (wave & 1) + 4 * h;
+  const int q = q0 + 32 * j + l32;
+  float v[8];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float4 s = red[((2 * i + j) * 4 + 2 * (wave & 1) + g) * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float4 o = red[(w * 16 + (2 * i + j) * 4 + 2 * (wave & 1) + g) * 64 + lane];
+      s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+    }
+    v[4 * g] = s.x; v[4 * g + 1] = s.y; v[4 * g + 2] = s.z; v[4 * g + 3] = s.w;
+  }
+  if constexpr (EPI == kStats) {
+    int at = -1;
+    if (a.logit != nullptr && q < nq) {
+      if (a.targets != nullptr) {
+        const int64_t t = (int64_t)a.targets[q] - a.target_first;
+        at = t >= 0 && t < np ? (int)t : -1;
+      } else {
+        at = a.token[q].target;
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int p = pw + 8 * (e >> 2) + (e & 3);
+      if (at >= 0 && p == at) a.logit[q] = v[e];
+      v[e] = p < np ? v[e] : -INFINITY;
+      top = fmaxf(top, v[e]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], a.scale, -ref));
+    sum += __shfl_xor(sum, 32);
+    __syncthreads();
+    float2* of = reinterpret_cast<float2*>(lds);         // [4 sixteens of rows][64 tokens]
+    if (h == 0) of[(2 * i + (wave & 1)) * 64 + 32 * j + l32] = make_float2(top, sum);
+    __syncthreads();
+    if (threadIdx.x < 64 && q0 + threadIdx.x < nq) {
+      float2 r = of[threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float2 o = of[64 * w + threadIdx.x];
+        const float m = fmaxf(r.x, o.x), base = m == -INFINITY ? 0.f : m;
+        r.y = r.y * __builtin_amdgcn_exp2f(r.x - base) + o.y * __builtin_amdgcn_exp2f(o.x - base);
+        r.x = m;
+      }
+      a.part[(int64_t)blockIdx.x * a.tokens + q0 + threadIdx.x] = r;
+    }
+  } else {
+    Token tk = {INFINITY, 0.f, 0.f, -1};
+    if (q < nq) tk = a.token[q];
+    const float inv = a.top[1], wa = tk.a * inv, wb = tk.b * inv;
+    const int rel = tk.target < 0 ? -1 : tk.target - a.first;
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int p = pw + 8 * (e >> 2) + (e & 3);
+      float z = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], a.scale, -tk.lse2));
+      z -= p == rel ? wb : 0.f;
+      v[e] = p < np ? z : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+    char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)blockIdx.x * a.rows_t + q) * 128 + 2 * (pw - p0);
+    *reinterpret_cast<u32x2*>(dz) = u32x2{o[0], o[1]};
+    *reinterpret_cast<u32x2*>(dz + 16) = u32x2{o[2], o[3]};
+  }
 }
 
 // ------------------------------------------------------------ token passes --
@@ -763,42 +940,54 @@ struct Cost {
 __host__ __device__ __forceinline__ Cost cost_of(int epi) {
   return epi == kStats ? Cost{3900, 1700} : epi == kDz ? Cost{12000, 6000} : epi == kDw ? Cost{11000, 5000} : Cost{5000, 3000};
 }
-__host__ __device__ __forceinline__ int rounds_of(int tiles) { return (tiles + 255) >> 8; }
+__host__ __device__ __forceinline__ float rounds_of(uint32_t tiles) { return (float)((tiles + 255) >> 8); }
 
 // How many tiles along P are large: whole rounds of them, or all; what is left
 // over in small ones, where it would fill half a round or less.
-__host__ __device__ __forceinline__ Plan plan_of(int epi, int np, int nq, int K) {
-  const int tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
+struct Timed {
+  Plan plan;
+  float time;
+};
+__host__ __device__ __forceinline__ Timed plan_of(int epi, int np, int nq, int K) {
+  const uint32_t tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
   const int pairs = K > 128 ? (K + 127) / 128 : 1;
   const Cost e = cost_of(epi);
-  const int64_t large = 3100 * (int64_t)pairs + e.el, small = 1850 * (int64_t)pairs + e.es;
-  const int full = (int)((int64_t)tp * tl / 256);
-  Plan best = {tp, 1};
-  int64_t least = -1;
-  for (int i = 0; i < 4; ++i) {
+  const float large = 3100.f * pairs + e.el, small = 1850.f * pairs + e.es;
+  const uint32_t full = tp * tl / 256;
+  Timed best = {{(int)tp, 1}, -1.f};
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
     // all, none, all whole rounds, all but one of them
-    const int m = i == 0 ? tp : i == 1 || tl == 0 ? 0 : (int)((int64_t)(full - (i - 2)) * 256 / tl);
-    if (m < 0) continue;
-    const int64_t t = rounds_of(m * tl) * large + rounds_of((tp - m) * ts) * small + (m > 0 && m < tp ? 3000 : 0);
-    if (least < 0 || t < least) {
-      least = t;
-      best.large = m;
-    }
+    if (i > 1 && (tl == 0 || full < i - 2)) continue;
+    const uint32_t m = i == 0 ? tp : i == 1 ? 0 : (full - (i - 2)) * 256 / tl;
+    const float t = rounds_of(m * tl) * large + rounds_of((tp - m) * ts) * small + (m > 0 && m < tp ? 3000.f : 0.f);
+    if (best.time < 0.f || t < best.time) best = {{(int)m, 1}, t};
   }
   return best;
 }
 
-// The input gradient's tile size and parts, choice i of 24: parts 1, 2, 3, 4,
-// 6, 8, 12, .. 64, every part's way to memory and back at 6.4 values a ns.
-__host__ __device__ __forceinline__ Plan dx_choice(int i, int np, int nq, int K, int64_t* time) {
+// A gradient's tile size and parts of its reduction, choice i of 24: parts 1,
+// 2, 3, 4, 6, 8, 12, .. 64, every part's way to memory and back at 5.1 TB/s.
+__host__ __device__ __forceinline__ Timed split_choice(int epi, int i, int np, int nq, int K) {
   const int k = i >> 1, s = k < 2 ? k + 1 : (k & 1 ? 4 : 3) << (k - 2) / 2;
-  const int pairs = K > 128 ? (K + 127) / 128 : 1, tp = (np + 255) / 256;
-  const Cost e = cost_of(kDx);
-  const int each = (pairs + s - 1) / s;
-  const int tiles = tp * (i & 1 ? (nq + 127) / 128 : (nq + 255) / 256) * s;
-  *time = rounds_of(tiles) * (i & 1 ? 1850 * (int64_t)each + e.es : 3100 * (int64_t)each + e.el) +
-          (int64_t)s * np * nq / 640;
-  return Plan{i & 1 ? 0 : tp, s};
+  const uint32_t pairs = K > 128 ? (K + 127) / 128 : 1, tp = (np + 255) / 256;
+  const Cost e = cost_of(epi);
+  const float each = (float)((pairs + s - 1) / s);
+  const uint32_t tiles = tp * (i & 1 ? (nq + 127) / 128 : (nq + 255) / 256);
+  const float rounds = ceilf((float)tiles * (float)s * (1.f / 256.f));
+  const float time = rounds * (i & 1 ? 1850.f * each + e.es : 3100.f * each + e.el) +
+                     (float)s * (float)np * (float)nq * (1.f / 640.f) + (epi == kDw && s > 1 ? 2000.f : 0.f);
+  return {{i & 1 ? 0 : (int)tp, s}, time};
+}
+// The best of them, found by a wave.
+__device__ __forceinline__ Plan split_plan(int epi, int np, int nq, int K, int most, int lane) {
+  Timed p = split_choice(epi, lane < 24 ? lane : 0, np, nq, K);
+  if (p.plan.splits > most) p.time = INFINITY;
+  float least = p.time;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) least = fminf(least, __shfl_xor(least, d));
+  const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(p.time == least));
+  return Plan{__builtin_amdgcn_readlane(p.plan.large, at), __builtin_amdgcn_readlane(p.plan.splits, at)};
 }
 
 enum { kPlanLogits = 0, kPlanDx = 1, kPlanDw = 2, kPlans = 3 };
@@ -809,11 +998,23 @@ enum { kPlanLogits = 0, kPlanDx = 1, kPlanDw = 2, kPlans = 3 };
 // writes all that.  With `pack` every workgroup goes through the tokens, and
 // packs its share of the rows of x (stride `ld`; nothing where all tokens count
 // and x's own rows start on 128 bytes): for short batches, one launch for two.
+// Eight tokens per thread and turn, so that a turn's loads are in flight
+// together.  flag: the teacher's, or NULL: looked up here.
 constexpr int kPlaceList = 64;         // rows of a workgroup's share
-__global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, const uint8_t* flag, int32_t* pos,
-                                                          int32_t* rows, int32_t* n, Token* token,
-                                                          Plan* plans, int32_t piece, int32_t splits,
-                                                          float* top, uint16_t* pack, int32_t ld) {
+constexpr int kPlaceFlags = 1024;      // tokens whose entries this kernel looks up itself
+struct PlaceArgs {
+  const uint8_t* flag;
+  int32_t* pos;
+  int32_t* rows;
+  int32_t* n;
+  Token* token;
+  Plan* plans;
+  float* top;                // backward: [2]
+  uint16_t* pack;
+  int32_t ld, piece, dx_splits, dw_splits;
+};
+template <int PER>       // tokens of a thread in a turn
+__global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, const PlaceArgs o) {
   __shared__ int counts[2][16];
   __shared__ float tops[16];
   __shared__ int list[kPlaceList];
@@ -821,57 +1022,104 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
   const bool head = blockIdx.x == 0;
   int base = 0, turn = 0;
   float most = 0.f;
-  for (int64_t b = 0; b < a.T; b += 1024, turn ^= 1) {
-    const int64_t t = b + threadIdx.x;
-    const bool in = t < a.T && (a.index != nullptr ? flag[t] != 0 : a.targets[t] >= 0);
-    const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
-    if (lane == 0) counts[turn][wave] = __popcll(mask);
+  for (int64_t b = 0; b < a.T; b += 1024 * PER, turn ^= 1) {
+    const int64_t t0 = b + (int64_t)threadIdx.x * PER;
+    bool in[PER];
+    int32_t target[PER];
+    float up[PER], lse[PER], dlse[PER];
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int64_t t = t0 + e;
+      const bool there = t < a.T;
+      target[e] = -1;
+      in[e] = false;
+      if (there) {
+        if (a.index == nullptr) {
+          target[e] = a.targets[t];
+          in[e] = target[e] >= 0;
+        } else if (o.flag != nullptr) {
+          in[e] = o.flag[t] != 0;
+        } else if (PER == 1) {
+          bool any = false;
+          for (int j = 0; j < a.k && !any; j += 8) {
+            int at[8];
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int64_t i = t * a.k + min(j + u, a.k - 1);
+              at[u] = a.index[i];
+              v[u] = teacher_value(a, i);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) any |= at[u] >= 0 && v[u] > -INFINITY;
+          }
+          in[e] = any;
+        }
+      }
+      if (head && there && a.dloss != nullptr) {
+        up[e] = a.dloss[t];
+        lse[e] = a.lse_in[t];
+        dlse[e] = a.dlse != nullptr ? a.dlse[t] : 0.f;
+      }
+      mine += in[e] ? 1 : 0;
+    }
+    int before = mine;                                  // of the wave, then exclusive
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(before, d);
+      if (lane >= d) before += v;
+    }
+    if (lane == 63) counts[turn][wave] = before;
     __syncthreads();
-    int before = base + __popcll(mask & ((1ull << lane) - 1)), all = 0;
+    before += base - mine;
+    int all = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
       const int v = counts[turn][w];
       if (w < wave) before += v;
       all += v;
     }
-    if (in && pack != nullptr && before % gridDim.x == blockIdx.x) list[before / gridDim.x] = (int)t;
-    if (head && t < a.T) pos[t] = in ? before : -1;
-    if (head && in) {
-      rows[before] = (int32_t)t;
-      Token k = {0.f, 0.f, 0.f, -1};
-      if (a.index == nullptr) {
-        const int64_t at = (int64_t)a.targets[t] - a.first;
-        k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int64_t t = t0 + e;
+      if (t >= a.T) continue;
+      if (in[e] && o.pack != nullptr && before % gridDim.x == blockIdx.x) list[before / gridDim.x] = (int)t;
+      if (head) {
+        o.pos[t] = in[e] ? before : -1;
+        if (in[e]) {
+          o.rows[before] = (int32_t)t;
+          Token k = {0.f, 0.f, 0.f, -1};
+          if (a.index == nullptr) {
+            const int64_t at = (int64_t)target[e] - a.first;
+            k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
+          }
+          if (a.dloss != nullptr) {
+            k.lse2 = (float)((double)lse[e] / a.unscale);
+            k.b = up[e] * (float)a.c;
+            k.a = a.dlse != nullptr ? k.b + dlse[e] : k.b;
+            most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
+          }
+          o.token[before] = k;
+        }
       }
-      if (a.dloss != nullptr) {
-        k.lse2 = (float)((double)a.lse_in[t] / a.unscale);
-        k.b = a.dloss[t] * (float)a.c;
-        k.a = a.dlse != nullptr ? k.b + a.dlse[t] : k.b;
-        most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
-      }
-      token[before] = k;
+      before += in[e] ? 1 : 0;
     }
     base += all;
   }
   if (head) {
-    if (threadIdx.x == 0) *n = base;
-    if (threadIdx.x == 960) plans[kPlanLogits] = plan_of(top == nullptr ? kStats : kDz, piece, base, (int)a.D);
-    if (top != nullptr) {
-      if (threadIdx.x == 896) plans[kPlanDw] = plan_of(kDw, (int)a.D, piece, base);
+    if (threadIdx.x == 0) *o.n = base;
+    if (threadIdx.x == 960)
+      o.plans[kPlanLogits] = plan_of(o.top == nullptr ? kStats : kDz, o.piece, base, (int)a.D).plan;
+    if (o.top != nullptr) {
       if (wave == 13) {
-        int64_t time;
-        Plan p = dx_choice(lane < 24 ? lane : 0, base, (int)a.D, piece, &time);
-        if (p.splits > splits) time = INT64_MAX;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-          const int64_t other = __shfl_xor(time, d);
-          const Plan q = {__shfl_xor(p.large, d), __shfl_xor(p.splits, d)};
-          if (other < time || (other == time && (q.splits < p.splits || (q.splits == p.splits && q.large > p.large)))) {
-            time = other;
-            p = q;
-          }
-        }
-        if (lane == 0) plans[kPlanDx] = p;
+        const Plan p = split_plan(kDx, base, (int)a.D, o.piece, o.dx_splits, lane);
+        if (lane == 0) o.plans[kPlanDx] = p;
+      }
+      if (wave == 14) {
+        Plan p = split_plan(kDw, (int)a.D, o.piece, base, o.dw_splits, lane);
+        if (p.splits == 1) p = plan_of(kDw, (int)a.D, o.piece, base).plan;
+        if (lane == 0) o.plans[kPlanDw] = p;
       }
       most = wave_max(most);
       if (lane == 0) tops[wave] = most;
@@ -880,16 +1128,16 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
         for (int w = 1; w < 16; ++w) most = fmaxf(most, tops[w]);
         // a weight past the range where its inverse is a normal number is left as it is
         const bool fit = most > 1e-37f && most < 1e37f;
-        top[0] = fit ? most : 1.f;
-        top[1] = fit ? 1.f / most : 1.f;
+        o.top[0] = fit ? most : 1.f;
+        o.top[1] = fit ? 1.f / most : 1.f;
       }
     }
   }
-  if (pack == nullptr || (base == a.T && ld == a.D)) return;
+  if (o.pack == nullptr || (base == a.T && o.ld == a.D)) return;
   __syncthreads();
   for (int i = wave; i * (int64_t)gridDim.x + blockIdx.x < base; i += 16) {
     const u32x4* from = reinterpret_cast<const u32x4*>(a.x + (int64_t)list[i] * a.D);
-    u32x4* to = reinterpret_cast<u32x4*>(pack + ((int64_t)i * gridDim.x + blockIdx.x) * ld);
+    u32x4* to = reinterpret_cast<u32x4*>(o.pack + ((int64_t)i * gridDim.x + blockIdx.x) * o.ld);
     for (int c = lane; c < a.D / 8; c += 64) to[c] = from[c];
   }
 }
@@ -912,13 +1160,13 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const uint16_t* x, const
 // logarithm, the reference and the difference from the logit are put together
 // in 64 bits: each is up to log V, their sum may be far smaller.
 template <int TT, int NT>
-__global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const int32_t* pos, const Plan* plan_at,
-                                                       const Plan plan, const float2* part,
+__global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const int32_t parts_, const Plan* plan_at,
+                                                       const int32_t* pos, const float2* part,
                                                        const float* logit, double* lse64) {
   __shared__ float2 got[NT / 64][TT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = threadIdx.x % TT;
   const int64_t t = (int64_t)blockIdx.x * TT + tok;
-  const int parts = parts_before((int)((a.V + 255) / 256), plan_at != nullptr ? plan_at->large : plan.large);
+  const int parts = plan_at != nullptr ? parts_before((int)((a.V + 255) / 256), plan_at->large) : parts_;
   int p = -1;
   if (t < a.T) p = pos != nullptr ? pos[t] : a.index != nullptr || a.targets[t] >= 0 ? (int)t : -1;
   float top = -INFINITY, sum = 0.f;
@@ -949,31 +1197,27 @@ __global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const i
   }
 }
 
-// Distillation: the logits of a token's entries and its loss.  One wave per
-// token, four entries at a time, 8 columns per lane and step.
-__global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a, const double* lse64) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (t >= a.T) return;
-  float q[kEntryLanes], lq[kEntryLanes], z[kEntryLanes];
-  int at[kEntryLanes];
-  const bool any = teacher_row(a, t, lane, q, lq, at);
+// The logits of the entries of one token whose rows of w are given (row, -1 for
+// none; entry 64 i + lane), four entries at a time, 8 columns per lane and
+// step; wave `part` of `of` takes its share of the fours.
+__device__ __forceinline__ void entry_logits(const HeadArgs& a, int64_t t, int lane,
+                                             const int (&row)[kEntryLanes], int part, int of,
+                                             float (&z)[kEntryLanes]) {
   const uint16_t* x = a.x + t * a.D;
+  int turn = 0;
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
     z[i] = 0.f;
-    // the entry's row of w, -1 where it has none here
-    const int64_t rel = at[i] < 0 ? -1 : (int64_t)at[i] - a.first;
-    const int row = rel >= 0 && rel < a.V ? (int)rel : -1;
-    uint64_t todo = __builtin_amdgcn_ballot_w64(row >= 0);
+    uint64_t todo = __builtin_amdgcn_ballot_w64(row[i] >= 0);
     while (todo != 0) {
       int j[4], r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         j[e] = todo != 0 ? __builtin_ctzll(todo) : j[0];      // (past the last one: the first again)
         todo &= todo - 1;
-        r[e] = __builtin_amdgcn_readlane(row, j[e]);
+        r[e] = __builtin_amdgcn_readlane(row[i], j[e]);
       }
+      if (turn++ % of != part) continue;
       float s[4] = {};
 #pragma unroll 2
       for (int d = 8 * lane; d < a.D; d += 512) {
@@ -998,28 +1242,104 @@ __global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a, con
       }
     }
   }
-  double loss = 0.0;
-  const double lse = any ? lse64[t] : 0.0;
+}
+
+__device__ __forceinline__ void entry_rows(const HeadArgs& a, const int (&at)[kEntryLanes],
+                                           int (&row)[kEntryLanes]) {
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
-    const int j = 64 * i + lane;
-    if (j < a.k) a.logits[t * a.k + j] = z[i];
-    if (any && q[i] > 0.f) loss += (double)q[i] * ((double)lq[i] + (lse - (double)z[i] * a.c));
+    const int64_t rel = at[i] < 0 ? -1 : (int64_t)at[i] - a.first;
+    row[i] = rel >= 0 && rel < a.V ? (int)rel : -1;
   }
+}
+
+// sum over the entries of q (log q + lse - c z), in 64 bits (see the join).
+__device__ __forceinline__ float entry_loss(const HeadArgs& a, const float (&q)[kEntryLanes],
+                                            const float (&lq)[kEntryLanes], const float (&z)[kEntryLanes],
+                                            double lse) {
+  double loss = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEntryLanes; ++i)
+    if (q[i] > 0.f) loss += (double)q[i] * ((double)lq[i] + (lse - (double)z[i] * a.c));
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) loss += __shfl_xor(loss, d);
+  return (float)loss;
+}
+
+// Distillation: the logits of a token's entries and its loss.  One wave per token.
+__global__ __launch_bounds__(256) void head_entries_kernel(const HeadArgs a, const double* lse64) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (t >= a.T) return;
+  float q[kEntryLanes], lq[kEntryLanes], z[kEntryLanes];
+  int at[kEntryLanes], row[kEntryLanes];
+  const bool any = teacher_row(a, t, lane, q, lq, at);
+  entry_rows(a, at, row);
+  entry_logits(a, t, lane, row, 0, 1, z);
+#pragma unroll
+  for (int i = 0; i < kEntryLanes; ++i)
+    if (64 * i + lane < a.k) a.logits[t * a.k + 64 * i + lane] = z[i];
+  const float loss = any ? entry_loss(a, q, lq, z, lse64[t]) : 0.f;
+  if (lane == 0) a.loss[t] = loss;
+}
+
+// Both in one for short batches: a workgroup per token, its waves sharing the
+// parts and then the entries.
+__global__ __launch_bounds__(512) void head_finish_kernel(const HeadArgs a, const int32_t parts, const Plan* plan_at,
+                                                          const int32_t* pos, const float2* part) {
+  __shared__ float2 got[8];
+  __shared__ float zs[64 * kEntryLanes];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  float q[kEntryLanes], lq[kEntryLanes], z[kEntryLanes];
+  int at[kEntryLanes], row[kEntryLanes];
+  const bool any = teacher_row(a, t, lane, q, lq, at);
+  const int count = plan_at != nullptr ? parts_before((int)((a.V + 255) / 256), plan_at->large) : parts;
+  const int p = !any ? -1 : pos != nullptr ? pos[t] : (int)t;
+  float top = -INFINITY, sum = 0.f;
+  auto join = [&](const float2 v) {
+    const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
+    sum = sum * __builtin_amdgcn_exp2f(top - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
+    top = m;
+  };
+  if (p >= 0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count; i += 512) join(part[(int64_t)i * a.T + p]);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) join(make_float2(__shfl_xor(top, d), __shfl_xor(sum, d)));
+  if (lane == 0) got[wave] = make_float2(top, sum);
+  if (threadIdx.x < 64 * kEntryLanes) zs[threadIdx.x] = 0.f;
+  __syncthreads();
+  entry_rows(a, at, row);
+  entry_logits(a, t, lane, row, wave, 8, z);
+#pragma unroll
+  for (int i = 0; i < kEntryLanes; ++i)
+    if (z[i] != 0.f) zs[64 * i + lane] = z[i];           // (each entry of one wave)
+  __syncthreads();
+  if (wave != 0) return;
+  for (int w = 1; w < 8; ++w) join(got[w]);
+  const double lse = any ? (double)top * a.unscale + log((double)sum) : 0.0;
+#pragma unroll
+  for (int i = 0; i < kEntryLanes; ++i) {
+    z[i] = zs[64 * i + lane];
+    if (64 * i + lane < a.k) a.logits[t * a.k + 64 * i + lane] = z[i];
+  }
+  const float loss = any ? entry_loss(a, q, lq, z, lse) : 0.f;
   if (lane == 0) {
-    a.loss[t] = (float)loss;
-    if (!any) a.lse[t] = 0.f;
+    a.loss[t] = loss;
+    a.lse[t] = (float)lse;
   }
 }
 
 // Distillation, backward: dz at the entries of a token, from their logits.
 // entry[j]: its place in w (-1: none here, or told by an earlier entry of the
-// same place, whose q then holds both), value[j]: a p - b q, in 16 bits.
+// same place, whose q then holds both), value[j]: a p - b q, in 16 bits.  With
+// dz (the whole vocabulary's) they are put there at once.
 __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a, const int32_t* pos,
                                                                 const Token* token, const float* top,
-                                                                int32_t* entry, uint16_t* value) {
+                                                                int32_t* entry, uint16_t* value,
+                                                                int64_t rows_t, uint16_t* dz) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.T) return;
@@ -1057,8 +1377,12 @@ __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a
       const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[t * a.k + j], a.scale, -k.lse2));
       bits = pack2(k.a * top[1] * pr - k.b * top[1] * sum[i], 0.f) & 0xffffu;
     }
-    entry[t * a.k + j] = where;
-    value[t * a.k + j] = (uint16_t)bits;
+    if (dz != nullptr) {
+      if (where >= 0) dz[((int64_t)(where >> 6) * rows_t + p) * 64 + (where & 63)] = (uint16_t)bits;
+    } else {
+      entry[t * a.k + j] = where;
+      value[t * a.k + j] = (uint16_t)bits;
+    }
   }
 }
 
@@ -1076,23 +1400,45 @@ __global__ __launch_bounds__(256) void head_entry_store_kernel(const int32_t* po
 }
 
 // dx[t] = top sum over the parts of dx32[part][place], one rounding; zeros for
-// tokens that do not count.  A thread per 8 columns.
-__global__ __launch_bounds__(256) void head_dx_kernel(const int32_t* pos, const float* dx32,
-                                                      const Plan* plan, int32_t pairs, int64_t rows_t,
-                                                      int64_t T, int32_t D, const float* top, uint16_t* dx) {
-  const int64_t total = T * (D / 8);
-  const int splits = min(plan->splits, pairs);
-  const float scale = top[0];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / (D / 8);
-    const int d = 8 * (int)(i - t * (D / 8));
-    const int p = pos[t];
+// tokens that do not count.  From workgroup dx_blocks on: dw, where its
+// reduction was in parts.  A thread per 8 columns.
+struct SumArgs {
+  const int32_t* pos;
+  const int32_t* n;
+  const Plan* plans;
+  const float* top;
+  const float* dx32;
+  const float* dw32;
+  uint16_t* dx;
+  uint16_t* dw;
+  int64_t T, V, rows_t;
+  int32_t D, pairs;            // pairs of stages of dx's reduction
+  unsigned dx_blocks, dw_blocks;
+};
+__global__ __launch_bounds__(256) void head_sum_kernel(const SumArgs a) {
+  const bool w = blockIdx.x >= a.dx_blocks;
+  const float scale = a.top[0];
+  int splits;
+  if (w) {
+    splits = min(a.plans[kPlanDw].splits, max(1, (*a.n + 127) >> 7));
+    if (splits <= 1) return;                             // it is written
+  } else {
+    splits = min(a.plans[kPlanDx].splits, a.pairs);
+  }
+  const int64_t per_row = a.D / 8, total = (w ? a.V : a.T) * per_row;
+  const int64_t step = (int64_t)(w ? a.dw_blocks : a.dx_blocks) * 256;
+  const float* parts = w ? a.dw32 : a.dx32;
+  const int64_t part = (w ? a.V : a.rows_t) * a.D;
+  for (int64_t i = (int64_t)(blockIdx.x - (w ? a.dx_blocks : 0)) * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t r = i / per_row;
+    const int d = 8 * (int)(i - r * per_row);
+    const int64_t p = w ? r : a.pos[r];
     u32x4 v = {0, 0, 0, 0};
     if (p >= 0) {
       float s[8] = {};
 #pragma unroll 4
       for (int k = 0; k < splits; ++k) {
-        const float4* f = reinterpret_cast<const float4*>(dx32 + (k * rows_t + p) * D + d);
+        const float4* f = reinterpret_cast<const float4*>(parts + k * part + p * a.D + d);
         const float4 lo = f[0], hi = f[1];
         s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
         s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
@@ -1100,7 +1446,7 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const int32_t* pos, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = pack2(s[2 * e] * scale, s[2 * e + 1] * scale);
     }
-    *reinterpret_cast<u32x4*>(dx + t * D + d) = v;
+    *reinterpret_cast<u32x4*>((w ? a.dw : a.dx) + r * a.D + d) = v;
   }
 }
 
@@ -1149,7 +1495,7 @@ Common take_common(Parts& w, int64_t T, int64_t D) {
 
 // Batches of so few tokens that there is little to leave out: the forward
 // takes them as they are, without the three passes before the product.
-constexpr int64_t kAsTheyAre = 256;
+constexpr int64_t kAsTheyAre = 128;
 
 struct Forward {
   Common c;
@@ -1180,17 +1526,24 @@ struct Backward {
   float* top;
   uint16_t* dz;
   float* dx32;
+  float* dw32;
   int32_t* entry;
   uint16_t* value;
   int64_t rows_t, piece;
-  int32_t splits;
+  int32_t dx_splits, dw_splits;
 };
 
-// Most parts of the input gradient's reduction: of at least 1024 steps each,
-// 256 MiB in all.
+// Most parts of the gradients' reductions: of at least 256 steps each, 256 MiB
+// in all; of dw's only where its tiles are few and the vocabulary one piece.
 int32_t dx_splits(int64_t T, int64_t D, int64_t piece) {
   int64_t s = (int64_t(1) << 26) / (up(T, 256) * D);
-  if (s > piece / 1024) s = piece / 1024;
+  if (s > piece / 256) s = piece / 256;
+  return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+int32_t dw_splits(int64_t T, int64_t V, int64_t D, int64_t piece) {
+  if (V > piece || ((D + 255) / 256) * ((V + 127) / 128) > 128) return 1;
+  int64_t s = (int64_t(1) << 26) / (V * D);
+  if (s > T / 256) s = T / 256;
   return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
@@ -1199,12 +1552,16 @@ Backward take_backward(Parts& w, int64_t T, int64_t V, int64_t D, int64_t k) {
   b.c = take_common(w, T, D);
   b.rows_t = up(T, 256);
   b.piece = piece_of(T, V);
-  b.splits = dx_splits(T, D, b.piece);
+  b.dx_splits = dx_splits(T, D, b.piece);
+  b.dw_splits = dw_splits(T, V, D, b.piece);
   b.top = w.take<float>(2);
   b.dz = w.take<uint16_t>(b.rows_t * b.piece);
-  b.dx32 = w.take<float>(b.splits * b.rows_t * D);
-  b.entry = w.take<int32_t>(T * k);
-  b.value = w.take<uint16_t>(T * k);
+  b.dx32 = w.take<float>(b.dx_splits * b.rows_t * D);
+  if (b.dw_splits > 1) b.dw32 = w.take<float>(b.dw_splits * V * D);
+  if (V > b.piece) {
+    b.entry = w.take<int32_t>(T * k);
+    b.value = w.take<uint16_t>(T * k);
+  }
   return b;
 }
 
@@ -1213,12 +1570,34 @@ unsigned blocks_for(int64_t items, int64_t per, int64_t most) {
   return (unsigned)(b < 1 ? 1 : b > most ? most : b);
 }
 
+template <class F>
+hipError_t allow_lds(F* kernel, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 template <int EPI>
 int run_nt(const NtArgs& a, hipStream_t s) {
-  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&nt_kernel<EPI>),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, Large::LDS);
+  static const hipError_t set = allow_lds(&nt_kernel<EPI>, Large::LDS);
   if (set != hipSuccess) return set;
   hipLaunchKernelGGL(nt_kernel<EPI>, dim3(256), dim3(512), Large::LDS, s, a);
+  return hipGetLastError();
+}
+
+// Whether the logits of these sizes go in tiles of 64 x 64: where one round of
+// them takes the place of fewer, longer ones.  (Forward in us by large or small
+// tiles and by these, 1 to 256 tokens: 256 tiles 10.0 -> 7.8 at D = 256, 48 ->
+// 26 at D = 4096; 512 tiles 11.8 -> 12.6 at D = 256, 54 -> 52 at D = 4096; 1024
+// tiles 12.5 -> 19.7 and 60 -> 93.)
+bool tile64(int64_t np, int64_t nq, int64_t K) {
+  const int64_t tiles = ((np + 255) / 256 * 4) * ((nq + 63) / 64);
+  return tiles <= 256 || (tiles <= 512 && K >= 1536);
+}
+template <int EPI>
+int run_tile64(const NtArgs& a, hipStream_t s) {
+  constexpr int kLds = 8 * 16 * 64 * 16;
+  static const hipError_t set = allow_lds(&tile64_kernel<EPI>, kLds);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL(tile64_kernel<EPI>, dim3((unsigned)((a.np + 255) / 256 * 4), (unsigned)((a.nq + 63) / 64)),
+                     dim3(512), kLds, s, a);
   return hipGetLastError();
 }
 
@@ -1229,20 +1608,33 @@ int run_nt(const NtArgs& a, hipStream_t s) {
   } while (0)
 
 // Which tokens count, their order and, packed, their rows of x.
-int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t splits, float* top, hipStream_t s) {
-  if (a.index != nullptr) {
+int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t dx_splits, int32_t dw_splits,
+                 float* top, hipStream_t s) {
+  PlaceArgs o{};
+  if (a.index != nullptr && a.T > kPlaceFlags) {
     hipLaunchKernelGGL(head_flags_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, c.flag);
     MG_RUN(hipGetLastError());
+    o.flag = c.flag;
   }
-  const int32_t ld = (int32_t)up(a.D, 64);
   const bool both = a.T <= 256 * kPlaceList;
-  hipLaunchKernelGGL(head_place_kernel, dim3(both ? blocks_for(a.T, 16, 256) : 1), dim3(1024), 0, s, a, c.flag,
-                     c.pos, c.rows, c.n, c.token, c.plans, (int32_t)piece, splits, top,
-                     both ? c.xc : nullptr, ld);
+  o.pos = c.pos;
+  o.rows = c.rows;
+  o.n = c.n;
+  o.token = c.token;
+  o.plans = c.plans;
+  o.top = top;
+  o.pack = both ? c.xc : nullptr;
+  o.ld = (int32_t)up(a.D, 64);
+  o.piece = (int32_t)piece;
+  o.dx_splits = dx_splits;
+  o.dw_splits = dw_splits;
+  const dim3 grid(both ? blocks_for(a.T, 16, 256) : 1);
+  if (a.T <= kPlaceFlags) hipLaunchKernelGGL(head_place_kernel<1>, grid, dim3(1024), 0, s, a, o);
+  else hipLaunchKernelGGL(head_place_kernel<8>, grid, dim3(1024), 0, s, a, o);
   MG_RUN(hipGetLastError());
   if (both) return hipSuccess;
   hipLaunchKernelGGL(head_pack_kernel, dim3(blocks_for(a.T, 4, 2048)), dim3(256), 0, s, a.x, c.rows, c.n,
-                     (int32_t)a.T, (int32_t)a.D, c.xc, ld);
+                     (int32_t)a.T, (int32_t)a.D, c.xc, o.ld);
   return hipGetLastError();
 }
 
@@ -1286,19 +1678,33 @@ int launch_head(const HeadArgs& a, hipStream_t s) {
   Parts w;
   w.base = static_cast<char*>(a.workspace);
   const Forward f = take_forward(w, a.T, a.V, a.D);
-  if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, nullptr, s));
+  if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, 1, nullptr, s));
   NtArgs g = logits_args(a, f.c, 0, a.V);
-  g.plan = plan_of(kStats, (int)a.V, (int)a.T, (int)a.D);
   g.targets = f.c.pos != nullptr ? nullptr : a.targets;
   g.part = f.part;
   g.logit = a.index == nullptr ? f.logit : nullptr;
-  MG_RUN(run_nt<kStats>(g, s));
+  const int tp = (int)((a.V + 255) / 256);
+  int parts;
+  if (tile64(a.V, a.T, a.D)) {
+    parts = parts_before(tp, 0);
+    g.plan_at = nullptr;
+    MG_RUN(run_tile64<kStats>(g, s));
+  } else {
+    g.plan = plan_of(kStats, (int)a.V, (int)a.T, (int)a.D).plan;
+    parts = parts_before(tp, g.plan.large);
+    MG_RUN(run_nt<kStats>(g, s));
+  }
+  if (a.index != nullptr && a.T < 1024) {
+    hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)a.T), dim3(512), 0, s, a, parts, g.plan_at, f.c.pos,
+                       f.part);
+    return hipGetLastError();
+  }
   if (a.T < 1024)
-    hipLaunchKernelGGL((head_join_kernel<1, 256>), dim3((unsigned)a.T), dim3(256), 0, s, a, f.c.pos, g.plan_at,
-                       g.plan, f.part, f.logit, f.lse64);
+    hipLaunchKernelGGL((head_join_kernel<1, 256>), dim3((unsigned)a.T), dim3(256), 0, s, a, parts, g.plan_at,
+                       f.c.pos, f.part, f.logit, f.lse64);
   else
     hipLaunchKernelGGL((head_join_kernel<16, 1024>), dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s, a,
-                       f.c.pos, g.plan_at, g.plan, f.part, f.logit, f.lse64);
+                       parts, g.plan_at, f.c.pos, f.part, f.logit, f.lse64);
   MG_RUN(hipGetLastError());
   if (a.index != nullptr) {
     hipLaunchKernelGGL(head_entries_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, f.lse64);
@@ -1318,20 +1724,25 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
   const Backward b = take_backward(w, a.T, a.V, a.D, a.index != nullptr ? a.k : 0);
   const int32_t T = (int32_t)a.T, D = (int32_t)a.D;
   const int64_t entries = a.index != nullptr ? a.T * a.k : 0;
-  MG_RUN(place_tokens(a, b.c, b.piece, b.splits, b.top, s));
-  if (entries > 0) {
-    hipLaunchKernelGGL(head_entry_values_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a,
-                       b.c.pos, b.c.token, b.top, b.entry, b.value);
-    MG_RUN(hipGetLastError());
-  }
+  const bool one = a.V <= b.piece;
+  MG_RUN(place_tokens(a, b.c, b.piece, b.dx_splits, b.dw_splits, b.top, s));
+  auto entry_values = [&](uint16_t* dz) {
+    hipLaunchKernelGGL(head_entry_values_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, b.c.pos,
+                       b.c.token, b.top, b.entry, b.value, b.rows_t, dz);
+    return (int)hipGetLastError();
+  };
+  if (entries > 0 && !one) MG_RUN(entry_values(nullptr));
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
     const int64_t count = a.V - v0 < b.piece ? a.V - v0 : b.piece;
     NtArgs g = logits_args(a, b.c, v0, count);
     g.top = b.top;
     g.dz = b.dz;
     g.rows_t = b.rows_t;
-    MG_RUN(run_nt<kDz>(g, s));
-    if (entries > 0) {
+    if (tile64(count, T, D)) MG_RUN(run_tile64<kDz>(g, s));
+    else MG_RUN(run_nt<kDz>(g, s));
+    if (entries > 0 && one) {
+      MG_RUN(entry_values(b.dz));
+    } else if (entries > 0) {
       hipLaunchKernelGGL(head_entry_store_kernel, dim3(blocks_for(entries, 256, 2048)), dim3(256), 0, s,
                          b.c.pos, b.entry, b.value, entries, a.k, (int32_t)v0, (int32_t)count, b.rows_t, b.dz);
       MG_RUN(hipGetLastError());
@@ -1344,36 +1755,48 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     h.gq = 4;
     h.top = b.top;
     h.rows_t = b.rows_t;
-    if (a.dx != nullptr) {
-      h.P = dz;
-      h.Q = {a.w + v0 * a.D, (uint32_t)D * 2u, 128u};
-      h.plan_at = b.c.plans + kPlanDx;
-      h.np = T;
-      h.nq = D;
-      h.K = (int32_t)count;
-      h.add = v0 > 0;
-      h.dx = b.dx32;
-      MG_RUN(run_nt<kDx>(h, s));
-    }
-    if (a.dw != nullptr) {
-      h.P = g.Q;
-      h.x_all = g.x_all;
-      h.Q = dz;
-      h.plan_at = b.c.plans + kPlanDw;
-      h.np = D;
-      h.nq = (int32_t)count;
-      h.K = T;
-      h.dw = a.dw + v0 * a.D;
-      MG_RUN(run_nt<kDw>(h, s));
-    }
-  }
-  if (a.dx != nullptr) {
-    const int64_t first = a.V < b.piece ? a.V : b.piece;
-    hipLaunchKernelGGL(head_dx_kernel, dim3(blocks_for(a.T * (D / 8), 256, 4096)), dim3(256), 0, s, b.c.pos,
-                       b.dx32, b.c.plans + kPlanDx, (int32_t)((first + 127) / 128), b.rows_t, a.T, D, b.top, a.dx);
+    NtArgs x = h;
+    x.P = dz;
+    x.Q = {a.w + v0 * a.D, (uint32_t)D * 2u, 128u};
+    x.plan_at = b.c.plans + kPlanDx;
+    x.np = T;
+    x.nq = D;
+    x.K = (int32_t)count;
+    x.add = v0 > 0;
+    x.dx = a.dx != nullptr ? b.dx32 : nullptr;
+    h.P = g.Q;
+    h.x_all = g.x_all;
+    h.Q = dz;
+    h.plan_at = b.c.plans + kPlanDw;
+    h.np = D;
+    h.nq = (int32_t)count;
+    h.K = T;
+    h.dw = a.dw != nullptr ? a.dw + v0 * a.D : nullptr;
+    h.dw_parts = b.dw32;
+    static const hipError_t set = allow_lds(&grads_kernel, Large::LDS);
+    if (set != hipSuccess) return set;
+    hipLaunchKernelGGL(grads_kernel, dim3(256), dim3(512), Large::LDS, s, x, h);
     MG_RUN(hipGetLastError());
   }
-  return hipSuccess;
+  SumArgs o{};
+  o.pos = b.c.pos;
+  o.n = b.c.n;
+  o.plans = b.c.plans;
+  o.top = b.top;
+  o.dx32 = b.dx32;
+  o.dw32 = b.dw32;
+  o.dx = a.dx;
+  o.dw = a.dw;
+  o.T = a.T;
+  o.V = a.V;
+  o.rows_t = b.rows_t;
+  o.D = D;
+  o.pairs = (int32_t)(((one ? a.V : b.piece) + 127) / 128);
+  if (a.dx != nullptr) o.dx_blocks = blocks_for(a.T * (D / 8), 256, 4096);
+  if (a.dw != nullptr && b.dw_splits > 1) o.dw_blocks = blocks_for(a.V * (D / 8), 256, 4096);
+  if (o.dx_blocks + o.dw_blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(head_sum_kernel, dim3(o.dx_blocks + o.dw_blocks), dim3(256), 0, s, o);
+  return hipGetLastError();
 }
 
 }  // namespace mg

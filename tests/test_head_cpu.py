@@ -134,7 +134,8 @@ def test_workspace_sizes():
         wide = -(-D // 64) * 64                       # packed rows of x start on 128 bytes
         assert 0 < fwd < 2 * T * wide + 40 * T + 16 * T * (V / 128 + 4) + 4096
         assert 0 < bwd < (1 << 31) + 12 * (T + 256) * D * 64 + (1 << 28) * 2 * D
-        assert L.mg_head_bwd_workspace(T, V, D, 64) >= bwd + 6 * 64 * T
+        # the entries' places and values are kept where the vocabulary goes in pieces
+        assert L.mg_head_bwd_workspace(T, V, D, 64) >= bwd + (6 * 64 * T if T * V > 1 << 28 else 0)
 
 
 def test_binding_refuses_before_any_launch():
