@@ -158,9 +158,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // in memory and a fragment is read by the LDS transpose loads: lane i of 16
 // addresses step i / 4 and values 4 (i % 4) .. + 3 and receives value i of four
 // steps.  Otherwise [32 M N rows][64 steps], read with 128-bit loads.
-// Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) of its eight;
-// strided, at c ^ 4 (row % 4) of 16, or c ^ 4 (row / 2 % 2) of eight, so that
-// the four steps of a transpose load lie in different quarters of the banks.
+// Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) ^ (row / 8 % 2)
+// of its eight, so that 16 rows read at one chunk touch every bank once (two
+// rows span them all); strided, at c ^ 4 (row % 4) of 16, or c ^ 4 (row / 2 % 2)
+// of eight, so that the four steps of a transpose load lie in different quarters.
+// A wave's two loads of a unit are 16 rows apart: the same chunk for a lane.
 template <bool RS, int M, int N>
 struct Side {
   static constexpr int U = 32 * M * N;          // rows (strided: values) of a unit
@@ -196,9 +198,10 @@ struct Side {
     } else {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        at[kk] = lds + (uint32_t)((w * 32 * M + l32) * 128) + (uint32_t)(((2 * kk + h) ^ (l32 & 7)) << 4);
-      row = (uint32_t)(8 * S * wave + (lane >> 3)) * stride;
-      chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7)) << 4);
+        at[kk] = lds + (uint32_t)((w * 32 * M + l32) * 128) +
+                 (uint32_t)(((2 * kk + h) ^ (l32 & 7) ^ ((l32 >> 3) & 1)) << 4);
+      row = (uint32_t)(8 * ((wave & 1) + S * (wave & ~1)) + (lane >> 3)) * stride;
+      chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7) ^ (wave & 1)) << 4);
     }
   }
   // Rows from o0 of n, steps from k0 (a multiple of 128).  Rows past the end
@@ -231,10 +234,11 @@ struct Side {
               (col >> 6) * step + HALF * (U / 64) * step + 2 * (col & 63);
         off |= first + BUF * 64 + kRows * s < left && HALF * U + col < most ? 0u : kOOB;
       } else {
-        off = min(row + (uint32_t)(8 * s + U * HALF) * stride, most) + chunk + BUF * step;
+        off = min(row + (uint32_t)(16 * s + U * HALF) * stride, most) + chunk + BUF * step;
         off |= (int)(chunk >> 1) + BUF * 64 < left ? 0u : kOOB;
       }
-      dma16(rsrc, lds + (2u * BUF + HALF) * BYTES + (uint32_t)(wave * S + s) * 1024u, off);
+      dma16(rsrc, lds + (2u * BUF + HALF) * BYTES +
+                      (RS ? (uint32_t)(wave * S + s) : (uint32_t)((wave & 1) + S * (wave & ~1) + 2 * s)) * 1024u, off);
     }
   }
   template <int HALF, int BUF>
@@ -741,19 +745,21 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
   const char* Q = static_cast<const char*>(nq == a.tokens ? a.x_all : a.Q.base);
   // rows past the end repeat the last one, steps past it are zeros
   const uint32_t mine = (uint32_t)(uintptr_t)(lds_char*)lds + (uint32_t)wave * 16384u;
-  const uint32_t r8 = lane >> 3, chunk = 16u * ((lane & 7) ^ r8);
+  const uint32_t r8 = lane >> 3, chunk = 16u * ((lane & 7) ^ r8);       // of even eights of rows
   const uint32_t most[2] = {(uint32_t)(min(64, np - p0) - 1) * a.P.stride, (uint32_t)(min(64, nq - q0) - 1) * a.Q.stride};
   const uint32_t stride[2] = {a.P.stride, a.Q.stride};
   const uint64_t base[2] = {reinterpret_cast<uint64_t>(a.P.base) + (uint64_t)p0 * a.P.stride,
                             reinterpret_cast<uint64_t>(Q) + (uint64_t)q0 * a.Q.stride};
   auto load = [&](int block) {
-    const uint32_t past = (int)(chunk >> 1) + 64 * block < K ? 0u : kOOB;
+    const uint32_t past[2] = {(int)(chunk >> 1) + 64 * block < K ? 0u : kOOB,
+                              (int)((chunk ^ 16u) >> 1) + 64 * block < K ? 0u : kOOB};
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       const i32x4 rsrc = make_rsrc(reinterpret_cast<const void*>(base[o] + 128 * (uint64_t)block), 0x7fffffffu);
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        dma16(rsrc, mine + 8192u * o + 1024u * r, (min((r8 + 8 * r) * stride[o], most[o]) + chunk) | past);
+        dma16(rsrc, mine + 8192u * o + 1024u * r,
+              (min((r8 + 8 * r) * stride[o], most[o]) + (chunk ^ (16u * (r & 1)))) | past[r & 1]);
     }
   };
   f32x16 acc[2][2] = {};
@@ -766,7 +772,8 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        f[i][kk] = *(lds_frag*)(uintptr_t)(mine + 4096u * i + 128u * l32 + (uint32_t)(((2 * kk + h) ^ (l32 & 7)) << 4));
+        f[i][kk] = *(lds_frag*)(uintptr_t)(mine + 4096u * i + 128u * l32 +
+                                           (uint32_t)(((2 * kk + h) ^ (l32 & 7) ^ ((l32 >> 3) & 1)) << 4));
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     if (b + 8 < blocks) load(b + 8);
