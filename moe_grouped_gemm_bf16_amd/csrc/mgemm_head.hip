@@ -36,6 +36,7 @@ namespace {
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -128,49 +129,50 @@ struct NtArgs {
   int32_t D;
 };
 
-// Tile of BP x BQ outputs, WP x WQ waves of (64 MH) x 64 each, 64 reduction
+// Tile of BP x BQ outputs, WP x WQ waves of (32 MB) x 64 each, 64 reduction
 // steps a stage, two stages in LDS.  Every operand tile is staged as two
-// units, its first half and its second; a wave holds 32 MH rows of each P half
-// and 32 of each Q half.  So a stage is four products of a P half and a Q half,
+// units, its first half and its second; a wave holds MB blocks of 16 rows of
+// each P half and two of each Q half.  So a stage is four products of a P half and a Q half,
 // and a unit can be refilled as soon as its fragments are in registers, while
 // the rest of the stage is still multiplied: a load has five of the eight
 // phases of two stages (1.3 us of 256 x 256 tiles) before its data are read.
-template <int MH_, int WP_, int WQ_>
+template <int MB_, int WP_, int WQ_>
 struct Cfg {
-  static constexpr int MH = MH_, WP = WP_, WQ = WQ_;
-  static constexpr int BP = WP * 64 * MH, BQ = WQ * 64;
+  static constexpr int MB = MB_, WP = WP_, WQ = WQ_;
+  static constexpr int BP = WP * 32 * MB, BQ = WQ * 64;
   static constexpr int UP = BP / 2 * 128, UQ = BQ / 2 * 128;     // bytes of a unit
   static constexpr int SP = BP / 2 / 64, SQ = BQ / 2 / 64;       // loads of a unit per wave
   static constexpr int LDS = 4 * (UP + UQ);
   static_assert(WP * WQ == 8 && SP >= 1 && SQ >= 1, "eight waves");
   static_assert(4 * UP <= 65536 && 4 * UQ <= 65536, "read offsets of 16 bits");
 };
-typedef Cfg<2, 2, 4> Large;      // 256 x 256
-typedef Cfg<1, 4, 2> Small;      // 256 x 128
+typedef Cfg<4, 2, 4> Large;      // 256 x 256
+typedef Cfg<2, 4, 2> Small;      // 256 x 128
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// One operand of the tile: N waves along it, each with M blocks of 32 rows in
-// either half; B waves' worth of LDS at `lds`.
-// RS (strided): the unit holds [64 reduction steps][32 M N] values as they lie
+// One operand of the tile: N waves along it, each with M blocks of 16 rows in
+// either half.
+// RS (strided): the unit holds [64 reduction steps][16 M N] values as they lie
 // in memory and a fragment is read by the LDS transpose loads: lane i of 16
 // addresses step i / 4 and values 4 (i % 4) .. + 3 and receives value i of four
-// steps.  Otherwise [32 M N rows][64 steps], read with 128-bit loads.
+// steps.  Otherwise [16 M N rows][64 steps], read with 128-bit loads.
 // Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) ^ (row / 8 % 2)
 // of its eight, so that 16 rows read at one chunk touch every bank once (two
-// rows span them all); strided, at c ^ 4 (row % 4) of 16, or c ^ 4 (row / 2 % 2)
-// of eight, so that the four steps of a transpose load lie in different quarters.
+// rows span them all).  Strided, 32 lanes read two chunks of steps 0-3 and 8-11:
+// at c ^ 2 (row % 4 + 4 (row / 8 % 2)) of 16, or c ^ 2 (row / 2 % 2 +
+// 2 (row / 8 % 2)) of eight, these lie in different places.
 // A wave's two loads of a unit are 16 rows apart: the same chunk for a lane.
 template <bool RS, int M, int N>
 struct Side {
-  static constexpr int U = 32 * M * N;          // rows (strided: values) of a unit
+  static constexpr int U = 16 * M * N;          // rows (strided: values) of a unit
   static constexpr int BYTES = U * 128;
   static constexpr int S = U / 64;              // loads of a unit per wave
-  static constexpr int kReads = RS ? 8 * M : 4 * M;
+  static constexpr int kReads = RS ? 4 * M : 2 * M;
   static_assert(U == 128 || U == 64, "row swizzle");
-  uint32_t at[RS ? M : 4];     // fragment addresses, by block or by slice of 16 steps
+  uint32_t at[RS ? M : 2];     // fragment addresses, by block or by slice of 32 steps
   uint32_t lds;                // the operand's first unit
   uint32_t row, chunk;         // load: byte offset of the lane's row; its chunk's bytes
   uint64_t base;
@@ -181,25 +183,26 @@ struct Side {
     lds = lds_;
     stride = o.stride;
     step = o.step;
-    const int l32 = lane & 31, h = lane >> 5;
+    const int i = lane & 15, g = lane >> 4;
     if constexpr (RS) {
-      const int i = lane & 15, g = (lane >> 4) & 1, r = 8 * h + (i >> 2);
-      const int swz = U == 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1);
+      const int r = 8 * g + (i >> 2);
+      const int swz = U == 128 ? (i >> 2) + 4 * (g & 1) : ((i >> 3) & 1) + 2 * (g & 1);
 #pragma unroll
       for (int b = 0; b < M; ++b) {
-        const int c = (4 * (w * M + b) + 2 * g + ((i & 3) >> 1)) ^ swz;
+        const int c = (2 * (w * M + b) + ((i & 3) >> 1)) ^ (2 * swz);
         at[b] = lds + (uint32_t)(r * U * 2 + 16 * c + 8 * (i & 1));
       }
       constexpr int kRow = U / 8;                              // chunks of a row
       const int lr = lane / kRow;                              // row within 1 KiB
       first = 64 / kRow * (wave * S) + lr;
       row = (uint32_t)first * stride;
-      chunk = 16u * (uint32_t)((lane % kRow) ^ (U == 128 ? 4 * (lr & 3) : 4 * ((lr >> 1) & 1)));
+      const int to = U == 128 ? (lr & 3) + 4 * (wave & 1) : ((lr >> 1) & 1) + 2 * (wave & 1);
+      chunk = 16u * (uint32_t)((lane % kRow) ^ (2 * to));
     } else {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        at[kk] = lds + (uint32_t)((w * 32 * M + l32) * 128) +
-                 (uint32_t)(((2 * kk + h) ^ (l32 & 7) ^ ((l32 >> 3) & 1)) << 4);
+      for (int kk = 0; kk < 2; ++kk)
+        at[kk] = lds + (uint32_t)((w * 16 * M + i) * 128) +
+                 (uint32_t)(((4 * kk + g) ^ (i & 7) ^ ((i >> 3) & 1)) << 4);
       row = (uint32_t)(8 * ((wave & 1) + S * (wave & ~1)) + (lane >> 3)) * stride;
       chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7) ^ (wave & 1)) << 4);
     }
@@ -242,19 +245,19 @@ struct Side {
     }
   }
   template <int HALF, int BUF>
-  __device__ __forceinline__ void read(bf16x8 (&f)[M][4]) const {
+  __device__ __forceinline__ void read(bf16x8 (&f)[M][2]) const {
     constexpr uint32_t unit = (2 * BUF + HALF) * BYTES;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int b = 0; b < M; ++b) {
         if constexpr (RS) {
-          const uint32_t a = at[b] + unit + kk * 16 * U * 2;
+          const uint32_t a = at[b] + unit + kk * 32 * U * 2;
           const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
           const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + 4 * U * 2));
           f[b][kk] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-          f[b][kk] = *(lds_frag*)(uintptr_t)(at[kk] + unit + b * 4096);
+          f[b][kk] = *(lds_frag*)(uintptr_t)(at[kk] + unit + b * 2048);
         }
       }
   }
@@ -262,10 +265,10 @@ struct Side {
 
 template <class C, bool PRS, bool QRS>
 struct Core {
-  f32x16 acc[2 * C::MH][2];
-  bf16x8 A0[C::MH][4], A1[C::MH][4], B0[1][4], B1[1][4];
-  Side<PRS, C::MH, C::WP> P;
-  Side<QRS, 1, C::WQ> Q;
+  f32x4 acc[2 * C::MB][4];
+  bf16x8 A0[C::MB][2], A1[C::MB][2], B0[2][2], B1[2][2];
+  Side<PRS, C::MB, C::WP> P;
+  Side<QRS, 2, C::WQ> Q;
   uint32_t live;
   int wave, left;
 
@@ -294,22 +297,28 @@ struct Core {
   template <int HALF, int BUF>
   __device__ __forceinline__ void loadQ() const { Q.template load<HALF, BUF>(live, left, wave); }
 
+  // 16 x 16 x 32 products: an accumulator is read and written once in 32 steps.
+  // (32 x 32 x 16 ones, once in 16, drew so much more power that the chip ran at
+  // 1.60 GHz, not 1.70, and kept the matrix cores 75% busy: 8192 x 131072 x 2048
+  // with the forward's epilogue 1275 TFLOP/s, with these 1404.)
   template <int HP, int HQ>
-  __device__ __forceinline__ void mul(const bf16x8 (&A)[C::MH][4], const bf16x8 (&B)[1][4]) {
+  __device__ __forceinline__ void mul(const bf16x8 (&A)[C::MB][2], const bf16x8 (&B)[2][2]) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-      for (int i = 0; i < C::MH; ++i)
-        acc[C::MH * HP + i][HQ] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            A[i][kk], B[0][kk], acc[C::MH * HP + i][HQ], 0, 0, 0);
+      for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[C::MB * HP + i][2 * HQ + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              A[i][kk], B[j][kk], acc[C::MB * HP + i][2 * HQ + j], 0, 0, 0);
   }
   // The reads between the products, evenly.
   template <int R>
   __device__ __forceinline__ void mix() {
-    constexpr int n = 4 * C::MH, each = (R + n - 1) / n;
+    constexpr int each = (R + 7) / 8;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, C::MB / 2, 0);
       if (i * each < R) __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -330,9 +339,9 @@ struct Core {
 
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 2 * C::MH; ++i)
+    for (int i = 0; i < 2 * C::MB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
   }
   __device__ __forceinline__ void start() {
     loadP<0, 0>(); loadQ<0, 0>(); loadQ<1, 0>(); loadP<1, 0>();
@@ -366,46 +375,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Two blocks of 32 x 32 results, 16 bits each, lane l holding of row l % 32
-// columns 8 g + 4 (l / 32) .. + 3 in x[2 g], x[2 g + 1], to 16 bytes of one row:
-// out[e] is of row (l % 32 & ~3) + e columns 8 (l % 4) .. + 7, of block a in
-// lanes 0-31 and of block b in lanes 32-63.  So a store writes 64 contiguous
-// bytes per row and block, where the registers as they are would give 16: the
-// stores' requests, not their bytes, are what an epilogue waits for (dz of 8192
-// x 131072, D = 4096: 7.0 -> 6.8 ms; dw of 96 tokens, V = 32768,
-// D = 2048: 48 -> 35 us).
-__device__ __forceinline__ void regroup(const uint32_t (&a)[8], const uint32_t (&b)[8], u32x4 (&out)[4],
-                                        int lane) {
-  uint32_t r[4][4];                  // [column group][dword]: the row's 16 bytes
+// Four blocks of 16 x 16 results, 16 bits each, lane l holding of row l % 16
+// and block b columns 4 (l / 16) .. + 3 in x[b], to 16 bytes of one row: out[e]
+// is of row (l % 16 & ~1) + e, block l / 16, columns 8 (l % 2) .. + 7.  So a
+// store writes up to 128 contiguous bytes per row, where the registers as they
+// are would give 32: the stores' requests, not their bytes, are what an
+// epilogue waits for (dw of 96 tokens, V = 32768, D = 2048: 48 -> 35 us when a
+// row's 16 bytes became 64).
+__device__ __forceinline__ void regroup(const u32x2 (&x)[4], u32x4 (&out)[2], int lane) {
+  uint32_t r[8];                     // block l / 16 of the lane's row, 16 columns
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
+  for (int d = 0; d < 2; ++d) {
+    // the other half wave's blocks, then the other 16 lanes' of each half
+    const auto a = __builtin_amdgcn_permlane32_swap(x[0][d], x[2][d], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(x[1][d], x[3][d], false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    r[d] = lo[0];
+    r[2 + d] = lo[1];
+    r[4 + d] = hi[0];
+    r[6 + d] = hi[1];
+  }
+  const bool odd = lane & 1;
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      // the upper half of a's register for the lower half of b's
-      const auto v = __builtin_amdgcn_permlane32_swap(a[2 * g + d], b[2 * g + d], false, false);
-      r[g][d] = v[0];
-      r[g][2 + d] = v[1];
-    }
-  // 4 x 4 transposes over the four lanes of a quad: with the neighbour, then
-  // with the lane two on
-  const bool odd = lane & 1, up = lane & 2;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    uint32_t t[4];
-#pragma unroll
-    for (int g = 0; g < 4; g += 2) {
-      const uint32_t x = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[g][d], 0xB1, 0xF, 0xF, true);
-      const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[g + 1][d], 0xB1, 0xF, 0xF, true);
-      t[g] = odd ? y : r[g][d];
-      t[g + 1] = odd ? r[g + 1][d] : x;
-    }
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint32_t x = (uint32_t)__builtin_amdgcn_mov_dpp((int)t[g], 0x4E, 0xF, 0xF, true);
-      const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)t[g + 2], 0x4E, 0xF, 0xF, true);
-      out[g][d] = up ? y : t[g];
-      out[g + 2][d] = up ? t[g + 2] : x;
-    }
+  for (int d = 0; d < 4; ++d) {      // second eight columns of the even row for the first of the odd one
+    const uint32_t u = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[d], 0xB1, 0xF, 0xF, true);
+    const uint32_t v = (uint32_t)__builtin_amdgcn_mov_dpp((int)r[4 + d], 0xB1, 0xF, 0xF, true);
+    out[0][d] = odd ? v : r[d];
+    out[1][d] = odd ? r[4 + d] : u;
   }
 }
 
@@ -475,12 +472,12 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   int nid = id;
   int left = aim(t, true) - 1;       // pairs until the loads move on to the next tile
   c.start();
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wp = c.wave / C::WQ, wq = c.wave % C::WQ;
-  constexpr int MP = 2 * C::MH;
-  // acc[i][j][4 g + e]: row P_ROW(i) + 8 g + 4 h + e of the wave's pw.., Q row
-  // qw + 32 wq + l32 + BQ / 2 j
-  auto p_row = [](int i) { return i / C::MH * (C::BP / 2) + 32 * (i % C::MH); };
+  constexpr int MP = 2 * C::MB;
+  // acc[i][j][e]: P row pw + p_row(i) + 4 g4 + e, Q row qw + q_row(j) + l16
+  auto p_row = [](int i) { return i / C::MB * (C::BP / 2) + 16 * (i % C::MB); };
+  auto q_row = [](int j) { return j / 2 * (C::BQ / 2) + 16 * (j % 2); };
 
   while (true) {
     int k0, m;
@@ -496,23 +493,23 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
       c.pair();
       --left;
     }
-    const int p0 = (tp0 + t.ip) * C::BP, pw = p0 + wp * 32 * C::MH, qw = t.iq * C::BQ + wq * 32;
+    const int p0 = (tp0 + t.ip) * C::BP, pw = p0 + wp * 16 * C::MB, qw = t.iq * C::BQ + wq * 32;
 
     if constexpr (EPI == kStats) {
       if (p0 + C::BP > np) {
-        const int rows = np - pw - 4 * h;
+        const int rows = np - pw - 4 * g4;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
-          for (int g = 0; g < 16; ++g)
-            if (p_row(i) + 8 * (g >> 2) + (g & 3) >= rows) {
-              c.acc[i][0][g] = -INFINITY;
-              c.acc[i][1][g] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (p_row(i) + e >= rows) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) c.acc[i][j][e] = -INFINITY;
             }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int q = qw + C::BQ / 2 * j + l32;
+      for (int j = 0; j < 4; ++j) {
+        const int q = qw + q_row(j) + l16;
         if (a.logit != nullptr) {
           int at = -1;
           if (q < nq) {
@@ -524,15 +521,14 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
             }
           }
           const int rel = at - pw;
-          const bool here = at >= 0 && rel >= 0 && rel < C::BP && ((rel >> 2) & 1) == h &&
-                            rel % (C::BP / 2) < 32 * C::MH;
+          const bool here = at >= 0 && rel >= 0 && rel < C::BP && ((rel >> 2) & 3) == g4 &&
+                            rel % (C::BP / 2) < 16 * C::MB;
           if (__builtin_amdgcn_ballot_w64(here) != 0) {
             float z = 0.f;
 #pragma unroll
             for (int i = 0; i < MP; ++i)
 #pragma unroll
-              for (int g = 0; g < 16; ++g)
-                z = rel - 4 * h == p_row(i) + 8 * (g >> 2) + (g & 3) ? c.acc[i][j][g] : z;
+              for (int e = 0; e < 4; ++e) z = rel - 4 * g4 == p_row(i) + e ? c.acc[i][j][e] : z;
             if (here) a.logit[q] = z;
           }
         }
@@ -540,20 +536,22 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
-          for (int g = 0; g < 16; ++g) top = fmaxf(top, c.acc[i][j][g]);
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, c.acc[i][j][e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
         const float ref = top == -INFINITY ? 0.f : top;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
-          for (int g = 0; g < 16; g += 2) {
-            s0 += __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][g], a.scale, -ref));
-            s1 += __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][g + 1], a.scale, -ref));
+          for (int e = 0; e < 4; e += 2) {
+            s0 += __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][e], a.scale, -ref));
+            s1 += __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i][j][e + 1], a.scale, -ref));
           }
         s0 += s1;
+        s0 += __shfl_xor(s0, 16);
         s0 += __shfl_xor(s0, 32);
-        if (h == 0 && q < nq) a.part[(int64_t)(part0 + t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
+        if (g4 == 0 && q < nq) a.part[(int64_t)(part0 + t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
       }
     }
 
@@ -561,72 +559,67 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
       const bool edge_p = p0 + C::BP > np;
       const float inv = a.top[1];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int q = qw + C::BQ / 2 * j + l32;
+      for (int j = 0; j < 4; ++j) {
+        const int q = qw + q_row(j) + l16;
         Token tk = {INFINITY, 0.f, 0.f, -1};
         if (q < nq) tk = a.token[q];
         const float wa = tk.a * inv, wb = tk.b * inv;
         const int rel = tk.target < 0 ? -1 : tk.target - a.first - pw;
         const bool told = __builtin_amdgcn_ballot_w64(rel >= 0 && rel < C::BP) != 0;
-        // block i of the lane's half after the regrouping, its four rows of dz
-        const int pb = pw + (lane < 32 ? 0 : p_row(1)), q4 = qw + C::BQ / 2 * j + (l32 & ~3);
-        char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)(pb >> 6) * a.rows_t + q4) * 128 +
-                   2 * (pb & 63) + 16 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < MP; i += 2) {
-          uint32_t pk[2][8];
+        for (int i = 0; i < MP; i += 4) {
+          u32x2 pk[4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            f32x16 v;
+          for (int u = 0; u < 4; ++u) {
+            float v[4];
 #pragma unroll
-            for (int g = 0; g < 16; ++g)
-              v[g] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i + u][j][g], a.scale, -tk.lse2));
-            if (told) {
-#pragma unroll
-              for (int g = 0; g < 16; ++g)
-                v[g] -= rel - 4 * h == p_row(i + u) + 8 * (g >> 2) + (g & 3) ? wb : 0.f;
-            }
-            if (edge_p) {
-#pragma unroll
-              for (int g = 0; g < 16; ++g)
-                v[g] = p_row(i + u) + 8 * (g >> 2) + (g & 3) < np - pw - 4 * h ? v[g] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              v[e] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i + u][j][e], a.scale, -tk.lse2));
+              if (told) v[e] -= rel - 4 * g4 == p_row(i + u) + e ? wb : 0.f;
+              if (edge_p) v[e] = p_row(i + u) + e < np - pw - 4 * g4 ? v[e] : 0.f;
             }
             // the one rounding of dz: a 16-bit operand of the two products
-#pragma unroll
-            for (int g = 0; g < 8; ++g) pk[u][g] = pack2(v[2 * g], v[2 * g + 1]);
-            __builtin_amdgcn_sched_barrier(0);    // a block's values at a time: registers
+            pk[u] = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
           }
-          u32x4 out[4];
-          regroup(pk[0], pk[1], out, lane);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x4*>(dz + 128 * e) = out[e];
-          dz += C::BP / 128 * a.rows_t * 128;     // (Large) the other half's blocks
-          __builtin_amdgcn_sched_barrier(0);
+          u32x4 out[2];
+          regroup(pk, out, lane);
+          // the lane's block, its two rows of dz
+          const int pb = pw + p_row(i) + (C::MB == 4 ? 16 * g4 : (g4 >> 1) * (C::BP / 2) + 16 * (g4 & 1));
+          char* dz = reinterpret_cast<char*>(a.dz) +
+                     ((int64_t)(pb >> 6) * a.rows_t + qw + q_row(j) + (l16 & ~1)) * 128 + 2 * (pb & 63) + 16 * (lane & 1);
+          *reinterpret_cast<u32x4*>(dz) = out[0];
+          *reinterpret_cast<u32x4*>(dz + 128) = out[1];
+          __builtin_amdgcn_sched_barrier(0);      // four blocks' values at a time: registers
         }
       }
     }
 
     if constexpr (EPI == kDx) {
-      // P = tokens, Q = hidden columns: 32 consecutive columns per half wave
+      // P = tokens, Q = hidden columns: 32 consecutive columns per row and store
       auto store = [&](auto whole, auto add) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = qw + C::BQ / 2 * j + l32;
-          const int rows = d < nq ? np - pw - 4 * h : 0;
-          float* to = a.dx + ((int64_t)t.s * a.rows_t + pw + 4 * h) * a.D + d;
+        for (int j = 0; j < 4; j += 2) {
+          const int d = qw + q_row(j) + 16 * (g4 & 1) + l16, p4 = pw + 4 * (g4 & ~1);
+          const int rows = d < nq ? np - p4 : 0;
+          float* to = a.dx + ((int64_t)t.s * a.rows_t + p4) * a.D + d;
 #pragma unroll
           for (int i = 0; i < MP; ++i) {
             asm volatile("" : "+v"(to));      // a block's addresses at a time: registers
             float* at = to + (int64_t)p_row(i) * a.D;
 #pragma unroll
-            for (int g = 0; g < 16; ++g) {
-              if (whole.value || p_row(i) + 8 * (g >> 2) + (g & 3) < rows) {
-                // (adding: once per element and launch, so there is no order to
-                // depend on, and no load to wait for)
-                if (add.value) unsafeAtomicAdd(at, c.acc[i][j][g]);
-                else *at = c.acc[i][j][g];
-              }
-              at += (g & 3) == 3 ? 5 * (int64_t)a.D : a.D;
+            for (int e = 0; e < 4; ++e) {
+              // rows 4 g4 + e of 16 columns each -> of 32: the even 16 lanes' row, the odd ones'
+              const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(c.acc[i][j][e]),
+                                                              __float_as_uint(c.acc[i][j + 1][e]), false, false);
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if (whole.value || p_row(i) + 4 * u + e < rows) {
+                  // (adding: once per element and launch, so there is no order to
+                  // depend on, and no load to wait for)
+                  float* here = at + (int64_t)(4 * u + e) * a.D;
+                  if (add.value) unsafeAtomicAdd(here, __uint_as_float(v[u]));
+                  else *here = __uint_as_float(v[u]);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -644,37 +637,33 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
       const float scale = a.top[0];
       if (splits > 1) {          // parts in fp32, joined by head_sum_kernel
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int q = qw + C::BQ / 2 * j + l32;
-          float* to = a.dw_parts + ((int64_t)t.s * nq + q) * a.D + pw + 4 * h;
+        for (int j = 0; j < 4; ++j) {
+          const int q = qw + q_row(j) + l16;
+          float* to = a.dw_parts + ((int64_t)t.s * nq + q) * a.D + pw + 4 * g4;
 #pragma unroll
           for (int i = 0; i < MP; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (q < nq && pw + p_row(i) + 8 * g < np)
-                *reinterpret_cast<float4*>(to + p_row(i) + 8 * g) =
-                    make_float4(c.acc[i][j][4 * g], c.acc[i][j][4 * g + 1], c.acc[i][j][4 * g + 2], c.acc[i][j][4 * g + 3]);
+            if (q < nq && pw + p_row(i) + 4 * g4 < np) *reinterpret_cast<f32x4*>(to + p_row(i)) = c.acc[i][j];
         }
-      } else
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int q4 = qw + C::BQ / 2 * j + (l32 & ~3);
+        for (int j = 0; j < 4; ++j) {
+          const int q2 = qw + q_row(j) + (l16 & ~1);
 #pragma unroll
-        for (int i = 0; i < MP; i += 2) {
-          uint32_t pk[2][8];
+          for (int i = 0; i < MP; i += 4) {
+            u32x2 pk[4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 4; ++u)
+              pk[u] = u32x2{pack2(c.acc[i + u][j][0] * scale, c.acc[i + u][j][1] * scale),
+                            pack2(c.acc[i + u][j][2] * scale, c.acc[i + u][j][3] * scale)};
+            u32x4 out[2];
+            regroup(pk, out, lane);
+            const int d = pw + p_row(i) + (C::MB == 4 ? 16 * g4 : (g4 >> 1) * (C::BP / 2) + 16 * (g4 & 1)) + 8 * (lane & 1);
+            uint16_t* to = a.dw + (int64_t)q2 * a.D + d;
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-              pk[u][g] = pack2(c.acc[i + u][j][2 * g] * scale, c.acc[i + u][j][2 * g + 1] * scale);
-          u32x4 out[4];
-          regroup(pk[0], pk[1], out, lane);
-          const int d = pw + (lane < 32 ? p_row(i) : p_row(i + 1)) + 8 * (lane & 3);
-          uint16_t* to = a.dw + (int64_t)q4 * a.D + d;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (q4 + e < nq && d < np) *reinterpret_cast<u32x4*>(to + (int64_t)e * a.D) = out[e];
-          __builtin_amdgcn_sched_barrier(0);
+            for (int e = 0; e < 2; ++e)
+              if (q2 + e < nq && d < np) *reinterpret_cast<u32x4*>(to + (int64_t)e * a.D) = out[e];
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
     }
