@@ -159,12 +159,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // in memory and a fragment is read by the LDS transpose loads: lane i of 16
 // addresses step i / 4 and values 4 (i % 4) .. + 3 and receives value i of four
 // steps.  Otherwise [16 M N rows][64 steps], read with 128-bit loads.
-// Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) ^ (row / 8 % 2)
-// of its eight, so that 16 rows read at one chunk touch every bank once (two
-// rows span them all).  Strided, 32 lanes read two chunks of steps 0-3 and 8-11:
+// Bank conflicts: 16-byte chunk c of a row lies at c ^ (row % 8) of its eight (a
+// 128-bit load takes lanes 0-3, 12-15, 20-23 and 24-27 together, which are then
+// in different places; two rows span the banks).  Strided, 32 lanes read two chunks of steps 0-3 and 8-11:
 // at c ^ 2 (row % 4 + 4 (row / 8 % 2)) of 16, or c ^ 2 (row / 2 % 2 +
 // 2 (row / 8 % 2)) of eight, these lie in different places.
-// A wave's two loads of a unit are 16 rows apart: the same chunk for a lane.
 template <bool RS, int M, int N>
 struct Side {
   static constexpr int U = 16 * M * N;          // rows (strided: values) of a unit
@@ -202,9 +201,9 @@ struct Side {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
         at[kk] = lds + (uint32_t)((w * 16 * M + i) * 128) +
-                 (uint32_t)(((4 * kk + g) ^ (i & 7) ^ ((i >> 3) & 1)) << 4);
-      row = (uint32_t)(8 * ((wave & 1) + S * (wave & ~1)) + (lane >> 3)) * stride;
-      chunk = (uint32_t)(((lane & 7) ^ ((lane >> 3) & 7) ^ (wave & 1)) << 4);
+                 (uint32_t)(((4 * kk + g) ^ (i & 7)) << 4);
+      row = (uint32_t)(8 * S * wave + (lane >> 3)) * stride;
+      chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
     }
   }
   // Rows from o0 of n, steps from k0 (a multiple of 128).  Rows past the end
@@ -237,11 +236,10 @@ struct Side {
               (col >> 6) * step + HALF * (U / 64) * step + 2 * (col & 63);
         off |= first + BUF * 64 + kRows * s < left && HALF * U + col < most ? 0u : kOOB;
       } else {
-        off = min(row + (uint32_t)(16 * s + U * HALF) * stride, most) + chunk + BUF * step;
+        off = min(row + (uint32_t)(8 * s + U * HALF) * stride, most) + chunk + BUF * step;
         off |= (int)(chunk >> 1) + BUF * 64 < left ? 0u : kOOB;
       }
-      dma16(rsrc, lds + (2u * BUF + HALF) * BYTES +
-                      (RS ? (uint32_t)(wave * S + s) : (uint32_t)((wave & 1) + S * (wave & ~1) + 2 * s)) * 1024u, off);
+      dma16(rsrc, lds + (2u * BUF + HALF) * BYTES + (uint32_t)(wave * S + s) * 1024u, off);
     }
   }
   template <int HALF, int BUF>
