@@ -1007,24 +1007,22 @@ struct PlaceArgs {
   uint16_t* pack;
   int32_t ld, piece, dx_splits, dw_splits;
 };
-template <int PER>       // tokens of a thread in a turn
+template <int PER>       // tokens of a thread in a turn, 1024 apart
 __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, const PlaceArgs o) {
-  __shared__ int counts[2][16];
+  __shared__ int counts[2][128];
   __shared__ float tops[16];
   __shared__ int list[kPlaceList];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool head = blockIdx.x == 0;
   int base = 0, turn = 0;
   float most = 0.f;
   for (int64_t b = 0; b < a.T; b += 1024 * PER, turn ^= 1) {
-    const int64_t t0 = b + (int64_t)threadIdx.x * PER;
     bool in[PER];
     int32_t target[PER];
     float up[PER], lse[PER], dlse[PER];
-    int mine = 0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int64_t t = t0 + e;
+      const int64_t t = b + 1024 * e + threadIdx.x;
       const bool there = t < a.T;
       target[e] = -1;
       in[e] = false;
@@ -1056,50 +1054,53 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
         lse[e] = a.lse_in[t];
         dlse[e] = a.dlse != nullptr ? a.dlse[t] : 0.f;
       }
-      mine += in[e] ? 1 : 0;
     }
-    int before = mine;                                  // of the wave, then exclusive
+    // places: by e, then wave, then lane
+    uint64_t mask[PER];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(before, d);
-      if (lane >= d) before += v;
+    for (int e = 0; e < PER; ++e) {
+      mask[e] = __builtin_amdgcn_ballot_w64(in[e]);
+      if (lane == 0) counts[turn][16 * e + wave] = __popcll(mask[e]);
     }
-    if (lane == 63) counts[turn][wave] = before;
     __syncthreads();
-    before += base - mine;
-    int all = 0;
+    int sum[2], total = 0;                     // counts before each (e, wave), 64 of them per register
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      const int v = counts[turn][w];
-      if (w < wave) before += v;
-      all += v;
+    for (int u = 0; u < 2; ++u) {
+      const int v = 64 * u + lane < 16 * PER ? counts[turn][64 * u + lane] : 0;
+      int s = v;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int w = __shfl_up(s, d);
+        if (lane >= d) s += w;
+      }
+      sum[u] = total + s - v;
+      total += __builtin_amdgcn_readlane(s, 63);
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int64_t t = t0 + e;
+      const int64_t t = b + 1024 * e + threadIdx.x;
+      const int before = base + __builtin_amdgcn_readlane(sum[e / 4], (16 * e + wave) & 63) +
+                         __popcll(mask[e] & ((1ull << lane) - 1));
       if (t >= a.T) continue;
       if (in[e] && o.pack != nullptr && before % gridDim.x == blockIdx.x) list[before / gridDim.x] = (int)t;
-      if (head) {
-        o.pos[t] = in[e] ? before : -1;
-        if (in[e]) {
-          o.rows[before] = (int32_t)t;
-          Token k = {0.f, 0.f, 0.f, -1};
-          if (a.index == nullptr) {
-            const int64_t at = (int64_t)target[e] - a.first;
-            k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
-          }
-          if (a.dloss != nullptr) {
-            k.lse2 = (float)((double)lse[e] / a.unscale);
-            k.b = up[e] * (float)a.c;
-            k.a = a.dlse != nullptr ? k.b + dlse[e] : k.b;
-            most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
-          }
-          o.token[before] = k;
-        }
+      if (!head) continue;
+      o.pos[t] = in[e] ? before : -1;
+      if (!in[e]) continue;
+      o.rows[before] = (int32_t)t;
+      Token k = {0.f, 0.f, 0.f, -1};
+      if (a.index == nullptr) {
+        const int64_t at = (int64_t)target[e] - a.first;
+        k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
       }
-      before += in[e] ? 1 : 0;
+      if (a.dloss != nullptr) {
+        k.lse2 = (float)((double)lse[e] / a.unscale);
+        k.b = up[e] * (float)a.c;
+        k.a = a.dlse != nullptr ? k.b + dlse[e] : k.b;
+        most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
+      }
+      o.token[before] = k;
     }
-    base += all;
+    base += total;
   }
   if (head) {
     if (threadIdx.x == 0) *o.n = base;
