@@ -923,16 +923,17 @@ __global__ __launch_bounds__(256) void head_flags_kernel(const HeadArgs a, uint8
   if (lane == 0) flag[t] = counts;
 }
 
-// The products' plans.  Times in ns: a tile of 256 x 256 takes 3100 per pair of
-// stages (128 steps), one of 256 x 128 1850, and its epilogue `el`, `es` more;
-// tiles run in rounds of the chip's 256 compute units.  (Measured on 2048
-// tokens, V = 65536, D = 512 to 2048, either size alone.  The epilogues that
-// write are the burst of all units' stores: 34 MB of dz in 8 us.)
+// The products' plans.  Times in ns: a tile of 256 x 256 takes 2800 per pair of
+// stages (128 steps), one of 256 x 128 1660 (2070 where w's rows do not start
+// on 128 bytes: its staged rows are then two reads of L2 each), and its epilogue
+// `el`, `es` more; tiles run in rounds of the chip's 256 compute units.
+// (Measured on 2048 tokens, V = 65536, D = 512 to 2064, either size alone.)
+constexpr float kLargePair = 2800.f, kSmallPair = 1660.f, kSmallPairOdd = 2070.f;
 struct Cost {
   int el, es;
 };
 __host__ __device__ __forceinline__ Cost cost_of(int epi) {
-  return epi == kStats ? Cost{3900, 1700} : epi == kDz ? Cost{12000, 6000} : epi == kDw ? Cost{11000, 5000} : Cost{5000, 3000};
+  return epi == kStats ? Cost{3600, 1900} : epi == kDz ? Cost{10000, 5500} : epi == kDw ? Cost{10000, 3000} : Cost{5000, 3000};
 }
 __host__ __device__ __forceinline__ float rounds_of(uint32_t tiles) { return (float)((tiles + 255) >> 8); }
 
@@ -946,7 +947,8 @@ __host__ __device__ __forceinline__ Timed plan_of(int epi, int np, int nq, int K
   const uint32_t tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
   const int pairs = K > 128 ? (K + 127) / 128 : 1;
   const Cost e = cost_of(epi);
-  const float large = 3100.f * pairs + e.el, small = 1850.f * pairs + e.es;
+  const float small_pair = (epi == kStats || epi == kDz) && K % 64 != 0 ? kSmallPairOdd : kSmallPair;
+  const float large = kLargePair * pairs + e.el, small = small_pair * pairs + e.es;
   const uint32_t full = tp * tl / 256;
   Timed best = {{(int)tp, 1}, -1.f};
 #pragma unroll
@@ -969,7 +971,7 @@ __host__ __device__ __forceinline__ Timed split_choice(int epi, int i, int np, i
   const float each = (float)((pairs + s - 1) / s);
   const uint32_t tiles = tp * (i & 1 ? (nq + 127) / 128 : (nq + 255) / 256);
   const float rounds = ceilf((float)tiles * (float)s * (1.f / 256.f));
-  const float time = rounds * (i & 1 ? 1850.f * each + e.es : 3100.f * each + e.el) +
+  const float time = rounds * (i & 1 ? kSmallPair * each + e.es : kLargePair * each + e.el) +
                      (float)s * (float)np * (float)nq * (1.f / 640.f) + (epi == kDw && s > 1 ? 2000.f : 0.f);
   return {{i & 1 ? 0 : (int)tp, s}, time};
 }
