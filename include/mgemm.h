@@ -235,17 +235,18 @@ mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float*
  *   loss[t]  = lse[t] - logit[t]
  * x: bf16 [T, D]; w: bf16 [V, D], the vocabulary entries first .. first + V - 1;
  * targets: int32 [T].  A token with a negative target does not count: its loss,
- * lse and logit are 0 (in a batch of more than 256 it costs no products).  loss, lse, logit:
+ * lse and logit are 0 (in a batch of more than 128 it costs no products).  loss, lse, logit:
  * fp32 [T] (written whole).  With the vocabulary in parts on several GPUs lse
  * and logit are a part's: the whole's lse is the log-sum-exp of theirs, its
  * logit their sum.  fp32 products and sums of exponentials, in a fixed order:
- * bitwise reproducible.  An infinite or NaN logit makes NaN in its token's loss
- * and no other's.
+ * bitwise reproducible.  A NaN or infinite logit makes its token's loss NaN or infinite
+ * and no other's; finite ones of any size do neither.
  * D a multiple of 8, 8 <= D <= 2^20; V >= 1 of any size, T <= 2^22; the count of
  * 256 x 128 tiles of z below 2^25, V D below 2^40; 0 <= first, first + V <= 2^31.  x, w 16-byte
  * aligned, the others 4-byte.  workspace: mg_head_workspace(T, V, D) bytes of
  * DEVICE memory, 16-byte aligned (no contents expected or kept); calls that may
- * run at the same time need one each.  T == 0 is a no-op.  Allocates nothing. */
+ * run at the same time need one each; no output may overlap an input.  T == 0 is
+ * a no-op.  Allocates nothing. */
 mg_status mg_head_loss(const void* x, const void* w, const int32_t* targets, int64_t T, int64_t V,
                        int64_t D, int64_t first, float* loss, float* lse, float* logit,
                        void* workspace, int64_t workspace_bytes, void* stream);
@@ -271,7 +272,7 @@ mg_status mg_head_distill(const void* x, const void* w, const void* teacher, int
                           void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of the workspace of mg_head_loss and mg_head_distill (0 for sizes that
- * they refuse). */
+ * they refuse): V T / 8, and for T > 128 2 T D, beside 40 T. */
 int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
 
 /* Gradient of mg_head_loss to x and w, from upstream gradients dloss (fp32
@@ -284,7 +285,8 @@ int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
  * that is not wanted costs nothing.  z is formed again, a piece of the
  * vocabulary at a time; dz is rounded to bf16 once, relative to the largest of
  * |dloss|, |dloss + dlse| (so that equal weights add no error of their own),
- * the products accumulate in fp32 and are rounded once.  Bitwise reproducible.
+ * the products accumulate in fp32 and are rounded once.  exp(z - lse) has the
+ * rounding of lse, 2^-24 |lse| relative, and is 1 at most.  Bitwise reproducible.
  * workspace: mg_head_bwd_workspace(T, V, D, 0) bytes.  T == 0 writes zero dw. */
 mg_status mg_head_loss_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
                            const float* dloss, const float* dlse, int64_t T, int64_t V, int64_t D,
@@ -302,8 +304,8 @@ mg_status mg_head_distill_bwd(const void* x, const void* w, const void* teacher,
                               void* dw, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of the workspace of the two gradients (k = 0: mg_head_loss_bwd; 0 for
- * sizes that they refuse): about 2 GiB at most for T up to 65536 beside what
- * grows with T D, dz being made for a piece of the vocabulary at a time. */
+ * sizes that they refuse): 6 T D and at most 1 GiB more for T up to 65536, dz
+ * being made for a piece of the vocabulary at a time. */
 int64_t mg_head_bwd_workspace(int64_t T, int64_t V, int64_t D, int32_t k);
 
 /* One group of mgemm_list: D [m, n] = A [m, k] B [n, k]^T (bf16 in and out,

@@ -573,7 +573,6 @@ mg_status head_backward(mg::HeadArgs& a, const int32_t* index, int64_t k, const 
 void head_temperature(mg::HeadArgs& a, double temperature) {
   a.c = 1.0 / temperature;
   a.scale = (float)(a.c * 1.44269504088896340736);
-  a.unscale = a.c / (double)a.scale;
 }
 
 mg::HeadArgs head_args(const void* x, const void* w, int64_t T, int64_t V, int64_t D, int64_t first) {

@@ -27,6 +27,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "mgemm_launch.h"
@@ -88,7 +89,7 @@ struct Operand {
 
 // A token that counts, as the backward's epilogue takes it.
 struct Token {
-  float lse2;           // lse log2(e)
+  float lse;            // lse / c, as the logits
   float a;              // weight of the probabilities
   float b;              // weight of the entries
   int32_t target;       // vocabulary entry of w, -1 for none or several (written apart)
@@ -116,7 +117,7 @@ struct NtArgs {
   int32_t first;            // logits: vocabulary entry of P's row 0 ...
   int64_t target_first;     // ... and, of targets[], of w's row 0
   float scale;              // logits: c log2(e)
-  float2* part;             // forward: [parts][T] (maximum, sum), base 2
+  float2* part;             // forward: [parts][T] (largest logit, sum of exponentials from it)
   float* logit;             // forward: logit of a token's target, or NULL
   const Token* token;       // logits: per counting token, or
   const int32_t* targets;   // (forward of all tokens) its target
@@ -135,7 +136,7 @@ struct NtArgs {
 // each P half and two of each Q half.  So a stage is four products of a P half and a Q half,
 // and a unit can be refilled as soon as its fragments are in registers, while
 // the rest of the stage is still multiplied: a load has five of the eight
-// phases of two stages (1.3 us of 256 x 256 tiles) before its data are read.
+// phases of two stages (1.7 us of 256 x 256 tiles) before its data are read.
 template <int MB_, int WP_, int WQ_>
 struct Cfg {
   static constexpr int MB = MB_, WP = WP_, WQ = WQ_;
@@ -404,6 +405,18 @@ __device__ __forceinline__ void regroup(const u32x2 (&x)[4], u32x4 (&out)[2], in
   }
 }
 
+// exp(c z - lse) is 2^(s z - r), one fma with s = c log2(e) and r = s lse / c
+// rounded; what r's rounding takes off, in all exponents alike, goes to the
+// factor before them.  Where r is past kFar that could be too much for a factor
+// and the difference is taken first (a branch of the whole wave, for such tokens).
+constexpr float kFar = 67108864.f;
+// z - lse, which is above 0 by lse's rounding only: p <= 1 however large z is.
+// (A comparison, so that NaN stays.)
+__device__ __forceinline__ float below(float z, float lse) {
+  const float d = z - lse;
+  return d > 0.f ? 0.f : d;
+}
+
 // A work item: tile (ip, iq) and, input gradient, part of the reduction.
 // Items run along P within groups of gq tiles of Q.
 struct Item {
@@ -536,8 +549,18 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = fmaxf(top, c.acc[i][j][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
-        const float ref = top == -INFINITY ? 0.f : top;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float ref = top == -INFINITY ? 0.f : top * a.scale;
+        const bool far = fabsf(ref) > kFar;
+        if (__builtin_amdgcn_ballot_w64(far) != 0) {
+          const float from = far ? top : 0.f;
+#pragma unroll
+          for (int i = 0; i < MP; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c.acc[i][j][e] -= from;
+          ref = far ? 0.f : ref;
+        }
+        const float off = far || top == -INFINITY ? 0.f : __builtin_fmaf(top, a.scale, -ref);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
@@ -549,6 +572,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
         s0 += s1;
         s0 += __shfl_xor(s0, 16);
         s0 += __shfl_xor(s0, 32);
+        s0 *= __builtin_amdgcn_exp2f(-off);
         if (g4 == 0 && q < nq) a.part[(int64_t)(part0 + t.ip * C::WP + wp) * a.tokens + q] = make_float2(top, s0);
       }
     }
@@ -559,9 +583,19 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int q = qw + q_row(j) + l16;
-        Token tk = {INFINITY, 0.f, 0.f, -1};
+        Token tk = {0.f, 0.f, 0.f, -1};
         if (q < nq) tk = a.token[q];
-        const float wa = tk.a * inv, wb = tk.b * inv;
+        const float wb = tk.b * inv;
+        float wa = tk.a * inv, ref = tk.lse * a.scale;
+        const bool far = fabsf(ref) > kFar;
+        if (__builtin_amdgcn_ballot_w64(far) != 0) {
+#pragma unroll
+          for (int i = 0; i < MP; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c.acc[i][j][e] = far ? below(c.acc[i][j][e], tk.lse) : c.acc[i][j][e];
+          ref = far ? 0.f : ref;
+        }
+        wa *= __builtin_amdgcn_exp2f(far ? 0.f : -__builtin_fmaf(tk.lse, a.scale, -ref));
         const int rel = tk.target < 0 ? -1 : tk.target - a.first - pw;
         const bool told = __builtin_amdgcn_ballot_w64(rel >= 0 && rel < C::BP) != 0;
 #pragma unroll
@@ -572,7 +606,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              v[e] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i + u][j][e], a.scale, -tk.lse2));
+              v[e] = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(c.acc[i + u][j][e], a.scale, -ref));
               if (told) v[e] -= rel - 4 * g4 == p_row(i + u) + e ? wb : 0.f;
               if (edge_p) v[e] = p_row(i + u) + e < np - pw - 4 * g4 ? v[e] : 0.f;
             }
@@ -814,11 +848,11 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
       v[e] = p < np ? v[e] : -INFINITY;
       top = fmaxf(top, v[e]);
     }
-    top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
-    const float ref = top == -INFINITY ? 0.f : top;
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float from = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], a.scale, -ref));
+    for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f((v[e] - from) * a.scale);
     sum += __shfl_xor(sum, 32);
     __syncthreads();
     float2* of = reinterpret_cast<float2*>(lds);         // [4 sixteens of rows][64 tokens]
@@ -830,13 +864,13 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
       for (int w = 1; w < 4; ++w) {
         const float2 o = of[64 * w + threadIdx.x];
         const float m = fmaxf(r.x, o.x), base = m == -INFINITY ? 0.f : m;
-        r.y = r.y * __builtin_amdgcn_exp2f(r.x - base) + o.y * __builtin_amdgcn_exp2f(o.x - base);
+        r.y = r.y * __builtin_amdgcn_exp2f((r.x - base) * a.scale) + o.y * __builtin_amdgcn_exp2f((o.x - base) * a.scale);
         r.x = m;
       }
       a.part[(int64_t)blockIdx.x * a.tokens + q0 + threadIdx.x] = r;
     }
   } else {
-    Token tk = {INFINITY, 0.f, 0.f, -1};
+    Token tk = {0.f, 0.f, 0.f, -1};
     if (q < nq) tk = a.token[q];
     const float inv = a.top[1], wa = tk.a * inv, wb = tk.b * inv;
     const int rel = tk.target < 0 ? -1 : tk.target - a.first;
@@ -844,7 +878,7 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int p = pw + 8 * (e >> 2) + (e & 3);
-      float z = wa * __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], a.scale, -tk.lse2));
+      float z = wa * __builtin_amdgcn_exp2f(below(v[e], tk.lse) * a.scale);
       z -= p == rel ? wb : 0.f;
       v[e] = p < np ? z : 0.f;
     }
@@ -1095,7 +1129,7 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
         k.target = at >= 0 && at < a.V ? (int32_t)at : -1;
       }
       if (a.dloss != nullptr) {
-        k.lse2 = (float)((double)lse[e] / a.unscale);
+        k.lse = (float)((double)lse[e] / a.c);
         k.b = up[e] * (float)a.c;
         k.a = a.dlse != nullptr ? k.b + dlse[e] : k.b;
         most = fmaxf(most, fmaxf(fabsf(k.a), fabsf(k.b)));
@@ -1169,7 +1203,7 @@ __global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const i
   float top = -INFINITY, sum = 0.f;
   auto join = [&](const float2 v) {
     const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
-    sum = sum * __builtin_amdgcn_exp2f(top - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
+    sum = sum * __builtin_amdgcn_exp2f((top - ref) * a.scale) + v.y * __builtin_amdgcn_exp2f((v.x - ref) * a.scale);
     top = m;
   };
   if (p >= 0) {
@@ -1182,7 +1216,7 @@ __global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const i
   __syncthreads();
   if (threadIdx.x >= TT || t >= a.T) return;
   for (int w = 1; w < NT / 64; ++w) join(got[w][threadIdx.x]);
-  const double lse = p >= 0 ? (double)top * a.unscale + log((double)sum) : 0.0;
+  const double lse = p >= 0 ? (double)top * a.c + log((double)sum) : 0.0;
   a.lse[t] = (float)lse;
   if (a.index != nullptr) {
     lse64[t] = lse;
@@ -1296,7 +1330,7 @@ __global__ __launch_bounds__(512) void head_finish_kernel(const HeadArgs a, cons
   float top = -INFINITY, sum = 0.f;
   auto join = [&](const float2 v) {
     const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
-    sum = sum * __builtin_amdgcn_exp2f(top - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
+    sum = sum * __builtin_amdgcn_exp2f((top - ref) * a.scale) + v.y * __builtin_amdgcn_exp2f((v.x - ref) * a.scale);
     top = m;
   };
   if (p >= 0) {
@@ -1316,7 +1350,7 @@ __global__ __launch_bounds__(512) void head_finish_kernel(const HeadArgs a, cons
   __syncthreads();
   if (wave != 0) return;
   for (int w = 1; w < 8; ++w) join(got[w]);
-  const double lse = any ? (double)top * a.unscale + log((double)sum) : 0.0;
+  const double lse = any ? (double)top * a.c + log((double)sum) : 0.0;
 #pragma unroll
   for (int i = 0; i < kEntryLanes; ++i) {
     z[i] = zs[64 * i + lane];
@@ -1371,7 +1405,7 @@ __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a
     if (any && at[i] >= 0 && !early[i] && at[i] >= a.first && at[i] - a.first < a.V) {
       where = (int)(at[i] - a.first);
       const Token k = token[p];
-      const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[t * a.k + j], a.scale, -k.lse2));
+      const float pr = __builtin_amdgcn_exp2f(below(a.logits_in[t * a.k + j], k.lse) * a.scale);
       bits = pack2(k.a * top[1] * pr - k.b * top[1] * sum[i], 0.f) & 0xffffu;
     }
     if (dz != nullptr) {
@@ -1567,14 +1601,29 @@ unsigned blocks_for(int64_t items, int64_t per, int64_t most) {
   return (unsigned)(b < 1 ? 1 : b > most ? most : b);
 }
 
+#define MG_RUN(call)                       \
+  do {                                     \
+    const int err_ = (call);               \
+    if (err_ != hipSuccess) return err_;   \
+  } while (0)
+
+// Lets a kernel have more than 64 KiB of LDS, once per device (`done`, a bit
+// for each; past 64 devices every time).
 template <class F>
-hipError_t allow_lds(F* kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+hipError_t allow_lds(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 template <int EPI>
 int run_nt(const NtArgs& a, hipStream_t s) {
-  static const hipError_t set = allow_lds(&nt_kernel<EPI>, Large::LDS);
-  if (set != hipSuccess) return set;
+  static std::atomic<uint64_t> done{0};
+  MG_RUN(allow_lds(&nt_kernel<EPI>, Large::LDS, done));
   hipLaunchKernelGGL(nt_kernel<EPI>, dim3(256), dim3(512), Large::LDS, s, a);
   return hipGetLastError();
 }
@@ -1591,18 +1640,12 @@ bool tile64(int64_t np, int64_t nq, int64_t K) {
 template <int EPI>
 int run_tile64(const NtArgs& a, hipStream_t s) {
   constexpr int kLds = 8 * 16 * 64 * 16;
-  static const hipError_t set = allow_lds(&tile64_kernel<EPI>, kLds);
-  if (set != hipSuccess) return set;
+  static std::atomic<uint64_t> done{0};
+  MG_RUN(allow_lds(&tile64_kernel<EPI>, kLds, done));
   hipLaunchKernelGGL(tile64_kernel<EPI>, dim3((unsigned)((a.np + 255) / 256 * 4), (unsigned)((a.nq + 63) / 64)),
                      dim3(512), kLds, s, a);
   return hipGetLastError();
 }
-
-#define MG_RUN(call)                       \
-  do {                                     \
-    const int err_ = (call);               \
-    if (err_ != hipSuccess) return err_;   \
-  } while (0)
 
 // Which tokens count, their order and, packed, their rows of x.
 int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t dx_splits, int32_t dw_splits,
@@ -1770,8 +1813,8 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     h.K = T;
     h.dw = a.dw != nullptr ? a.dw + v0 * a.D : nullptr;
     h.dw_parts = b.dw32;
-    static const hipError_t set = allow_lds(&grads_kernel, Large::LDS);
-    if (set != hipSuccess) return set;
+    static std::atomic<uint64_t> done{0};
+    MG_RUN(allow_lds(&grads_kernel, Large::LDS, done));
     hipLaunchKernelGGL(grads_kernel, dim3(256), dim3(512), Large::LDS, s, x, h);
     MG_RUN(hipGetLastError());
   }

@@ -152,8 +152,7 @@ struct HeadArgs {
   const int32_t* index;       // [T, k], or NULL: cross entropy
   int32_t k, teacher_bf16;
   double c;                   // 1 / temperature (1 for cross entropy)
-  float scale;                // c log2(e), rounded, and ...
-  double unscale;             // ... c / scale
+  float scale;                // c log2(e)
   float* loss;                // forward: [T]
   float* lse;                 // [T]
   float* logits;              // [T] or [T, k]

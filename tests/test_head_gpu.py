@@ -449,3 +449,100 @@ def test_through_a_layer_and_both_losses():
     for name, got, leaf in (("h", dh, leaves[0]), ("we", dwe, leaves[1]), ("w", dw, leaves[2])):
         off = (got.cpu().double() - leaf.grad).norm() / leaf.grad.norm()
         assert off <= 5 * 2.0 ** -8, (name, float(off))
+
+
+# the weights' gradient in parts over the tokens; the last sizes that go in 64 x
+# 64 tiles and the first that do not; large and small tiles in one product
+@pytest.mark.parametrize("T,V,D", [(6000, 700, 200), (3971, 1798, 352), (20000, 130, 72), (64, 16384, 72), (65, 8192, 1544), (65, 16384, 1544),
+                                   (65, 16640, 1544), (1333, 50001, 72), (2050, 3333, 1544), (129, 300, 64), (128, 300, 72)])
+def test_loss_by_every_cut(T, V, D):
+    _loss_case(T, V, D, ignored=0.05, z_loss=True, seed=V, uniform=False)
+
+
+@pytest.mark.parametrize("T,V,D", [(200, 1500, 64), (1500, 9000, 136)])
+@pytest.mark.parametrize("tau", [None, 1.0, 1e-6])
+def test_logits_of_any_size(T, V, D, tau):
+    """Rows of x from 1e-3 to 1e30: the losses stay finite and near, and where
+    one entry has all the probability the gradient is the difference of two rows
+    of w."""
+    g, x, w = _inputs(T, V, D, 70)
+    x = (x.float() * torch.logspace(-3, 30, T, device=DEV)[:, None]).bfloat16()
+    z = x.double() @ w.double().T
+    best = z.argmax(1).int()
+    t = torch.where(torch.arange(T, device=DEV) % 2 == 0, best, _targets(g, T, V, 0.0))
+    up = torch.randn(T, device=DEV, generator=g)
+    if tau is None:
+        r, e, c = mg.head_loss(x, w, t), ref.entries(targets=t), 1.0
+        dx, dw = mg.head_loss_bwd(x, w, t, r.lse, up)
+    else:
+        index, teacher, c = t[:, None].contiguous(), torch.zeros(T, 1, device=DEV), 1.0 / tau
+        r = mg.head_distill(x, w, teacher, index, temperature=tau)
+        e = ref.entries(teacher=teacher, index=index, temperature=tau)
+        dx, dw = mg.head_distill_bwd(x, w, teacher, index, r.lse, r.logits, up, temperature=tau)
+    loss, lse, _, tl, ts, _ = ref.forward(x, w, *e, temperature=1.0 / c)
+    _near("lse", r.lse, lse, ts)
+    _near("loss", r.loss, loss, tl)
+    assert dx.isfinite().all() and dw.isfinite().all()
+    top = z.topk(2, 1).values
+    alone = c * (top[:, 0] - top[:, 1]) > 1e-3 * c * top[:, 0].abs() + 100.0
+    assert alone.sum() > T / 3
+    # p <= 1 is of lse as it was rounded: dx lies between -w[t] and w[best] - w[t]
+    wb, wt, s = w[best.long()].double(), w[t.long()].double(), (c * up.double())[:, None]
+    ends = torch.stack((-s * wt, s * (wb - wt)))
+    slack = 2.0 ** -6 * s.abs() * (wb.abs() + wt.abs())
+    inside = (dx.double() >= ends.amin(0) - slack) & (dx.double() <= ends.amax(0) + slack)
+    assert inside[alone].all()
+    if tau is None:
+        # and lse is the largest logit itself, its p one (dz and dx rounded once each).
+        # (Distillation sums an entry's logit in another order: 66 u sum |x w| off,
+        # at |z| >= 2^26 = kFar more than an exponent of 1, so p is anything up to 1.)
+        assert ((dx.double() - s * (wb - wt)).abs() <= slack)[alone].all()
+
+
+def test_gradients_against_differences():
+    """dx and dw along a direction against the losses' central differences.  The
+    steps are exact in bf16; f(1/2) - f(-1/2) = f'(0) + f'''/24, and the third
+    derivative of a token's lse along dz is its third cumulant, at most the cube
+    of dz's range (of the loss and of lse alike)."""
+    T, V, D = 40, 300, 64
+    g = torch.Generator(device=DEV).manual_seed(71)
+    x = ((torch.randn(T, D, device=DEV, generator=g) * 8).round().clamp(-24, 24) / 8).bfloat16()
+    w = ((torch.randn(V, D, device=DEV, generator=g) * 8).round().clamp(-28, 28) / 64).bfloat16()
+    t = _targets(g, T, V, 0.2)
+    up, ul = torch.randn(T, device=DEV, generator=g), torch.randn(T, device=DEV, generator=g)
+    r = mg.head_loss(x, w, t)
+    e = ref.entries(targets=t)
+    dx, dw = mg.head_loss_bwd(x, w, t, r.lse, up, dlse=ul)
+    _, _, tx, tw = ref.backward(x, w, *e, r.lse, up, up.double() + ul.double())
+    weight = up.double().abs() + ul.double().abs()
+    for name, grad, tol, h in (("dx", dx, tx, 1 / 64), ("dw", dw, tw, 1 / 512)):
+        base = x if name == "dx" else w
+        for _ in range(8):
+            d = h * (torch.randint(0, 2, base.shape, device=DEV, generator=g) * 2 - 1).double()
+            sides, slack = [], 0.0
+            for sign in (1.0, -1.0):
+                at = (base.double() + sign * d).bfloat16()
+                assert torch.equal(at.double(), base.double() + sign * d)
+                a, b = (at, w) if name == "dx" else (x, at)
+                s = mg.head_loss(a, b, t)
+                _, _, _, tl, ts, _ = ref.forward(a, b, *e)
+                sides.append(((up.double() * s.loss.double()).sum() + (ul.double() * s.lse.double()).sum(), a.double() @ b.double().T))
+                slack += float((weight * torch.maximum(tl, ts)).sum())
+            dz = sides[0][1] - sides[1][1]
+            third = float((weight * (dz.amax(1) - dz.amin(1)) ** 3)[t >= 0].sum()) / 24
+            want, got = float(sides[0][0] - sides[1][0]), float((grad.double() * 2 * d).sum())
+            assert abs(got - want) <= slack + third + float((tol * 2 * d.abs()).sum()), (name, got, want)
+
+
+def test_misaligned_tensors_are_refused():
+    T, V, D = 10, 50, 64
+    g, x, w = _inputs(T, V, D, 72)
+    t = _targets(g, T, V, 0.0)
+    off = torch.empty(T * D + 4, dtype=torch.bfloat16, device=DEV)[4:].view(T, D)
+    off.copy_(x)
+    r = mg.head_loss(x, w, t)
+    for call in (lambda: mg.head_loss(off, w, t),
+                 lambda: mg.head_loss_bwd(off, w, t, r.lse, r.loss),
+                 lambda: mg.head_loss_bwd(x, w, t, r.lse, r.loss, dx=off)):
+        with pytest.raises(mg.MgemmError):
+            call()
