@@ -100,7 +100,8 @@ enum { kStats = 0, kDz = 1, kDx = 2, kDw = 3 };
 // How a product's tiles are cut, by the number of tokens that count.
 struct Plan {
   int32_t large;        // tiles along P of 256 x 256, the others of 256 x 128
-  int32_t splits;       // parts of the reduction (input gradient)
+  int32_t splits;       // parts of the reduction (gradients)
+  int32_t rows;         // rows of P that a small tile takes: 256, or fewer (logits)
 };
 
 struct NtArgs {
@@ -439,9 +440,11 @@ __device__ __forceinline__ Item item_of(int id, int tp, int tq, int gq) {
 // share operand rows in its L2.
 template <int EPI, class C>
 __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const int tp0, const int tp_end,
-                                         const int most_splits, const int part0, char* lds) {
+                                         const int most_splits, const int rows, const int part0, char* lds) {
   constexpr bool kSplit = EPI == kDx || EPI == kDw;
   constexpr bool kLogits = EPI == kStats || EPI == kDz;
+  constexpr bool kCut = kLogits && C::BQ < 256;       // tiles may take fewer rows of P
+  const int own = kCut ? rows : 256;
   const int np = EPI == kDx ? n_tok : a.np;
   const int nq = kLogits ? n_tok : a.nq;
   const int K = EPI == kDw ? n_tok : a.K;
@@ -476,7 +479,8 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   auto aim = [&](const Item& t, bool live) {
     int k0, m;
     range(t, k0, m);
-    c.source(Pp, Qp, live, (tp0 + t.ip) * C::BP, np, t.iq * C::BQ, nq, 128 * k0, K);
+    const int p0 = (tp0 + t.ip) * own;
+    c.source(Pp, Qp, live, p0, kCut ? min(np, p0 + own) : np, t.iq * C::BQ, nq, 128 * k0, K);
     return m;
   };
   Item t = item_of(id, tp, tq, a.gq), ahead = t;
@@ -504,11 +508,11 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
       c.pair();
       --left;
     }
-    const int p0 = (tp0 + t.ip) * C::BP, pw = p0 + wp * 16 * C::MB, qw = t.iq * C::BQ + wq * 32;
+    const int p0 = (tp0 + t.ip) * own, p_end = kCut ? min(np, p0 + own) : np, pw = p0 + wp * 16 * C::MB, qw = t.iq * C::BQ + wq * 32;
 
     if constexpr (EPI == kStats) {
-      if (p0 + C::BP > np) {
-        const int rows = np - pw - 4 * g4;
+      if (p0 + C::BP > p_end) {
+        const int rows = p_end - pw - 4 * g4;
 #pragma unroll
         for (int i = 0; i < MP; ++i)
 #pragma unroll
@@ -532,7 +536,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
             }
           }
           const int rel = at - pw;
-          const bool here = at >= 0 && rel >= 0 && rel < C::BP && ((rel >> 2) & 3) == g4 &&
+          const bool here = at >= 0 && rel >= 0 && (kCut ? at < p_end : rel < C::BP) && ((rel >> 2) & 3) == g4 &&
                             rel % (C::BP / 2) < 16 * C::MB;
           if (__builtin_amdgcn_ballot_w64(here) != 0) {
             float z = 0.f;
@@ -619,8 +623,10 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
           const int pb = pw + p_row(i) + (C::MB == 4 ? 16 * g4 : (g4 >> 1) * (C::BP / 2) + 16 * (g4 & 1));
           char* dz = reinterpret_cast<char*>(a.dz) +
                      ((int64_t)(pb >> 6) * a.rows_t + qw + q_row(j) + (l16 & ~1)) * 128 + 2 * (pb & 63) + 16 * (lane & 1);
-          *reinterpret_cast<u32x4*>(dz) = out[0];
-          *reinterpret_cast<u32x4*>(dz + 128) = out[1];
+          if (!kCut || pb < p_end) {
+            *reinterpret_cast<u32x4*>(dz) = out[0];
+            *reinterpret_cast<u32x4*>(dz + 128) = out[1];
+          }
           __builtin_amdgcn_sched_barrier(0);      // four blocks' values at a time: registers
         }
       }
@@ -710,9 +716,12 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
   asm volatile("" ::: "memory");
 }
 
-// Parts of the forward's sums before tile ip along P.
+// Parts of the forward's sums: before tile ip along P, and of all its tiles.
 __host__ __device__ __forceinline__ int parts_before(int ip, int large) {
   return ip < large ? ip * Large::WP : large * Large::WP + (ip - large) * Small::WP;
+}
+__host__ __device__ __forceinline__ int parts_of(int64_t V, const Plan& p) {
+  return parts_before((int)((V + p.rows - 1) / p.rows), p.large);
 }
 
 template <int EPI>
@@ -722,10 +731,12 @@ __device__ __forceinline__ void product(const NtArgs& a, char* lds) {
   if (a.plan_at != nullptr) {
     plan.large = __builtin_amdgcn_readfirstlane(a.plan_at->large);
     plan.splits = __builtin_amdgcn_readfirstlane(a.plan_at->splits);
+    if (EPI == kStats || EPI == kDz) plan.rows = __builtin_amdgcn_readfirstlane(a.plan_at->rows);
   }
-  const int tp = ((EPI == kDx ? n : a.np) + 255) / 256, large = min(plan.large, tp);
-  products<EPI, Large>(a, n, 0, large, plan.splits, 0, lds);
-  products<EPI, Small>(a, n, large, tp, plan.splits, parts_before(large, large), lds);
+  const int tp = EPI == kStats || EPI == kDz ? (a.np + plan.rows - 1) / plan.rows : ((EPI == kDx ? n : a.np) + 255) / 256;
+  const int large = min(plan.large, tp);
+  products<EPI, Large>(a, n, 0, large, plan.splits, plan.rows, 0, lds);
+  products<EPI, Small>(a, n, large, tp, plan.splits, plan.rows, parts_before(large, large), lds);
 }
 
 template <int EPI>
@@ -977,21 +988,32 @@ struct Timed {
   Plan plan;
   float time;
 };
-__host__ __device__ __forceinline__ Timed plan_of(int epi, int np, int nq, int K) {
+constexpr int kFewTokens = 128, kLeastRows = 64;
+__host__ __device__ __forceinline__ Timed plan_of(int epi, int np, int nq, int K, bool few) {
   const uint32_t tp = (np + 255) / 256, tl = (nq + 255) / 256, ts = (nq + 127) / 128;
   const int pairs = K > 128 ? (K + 127) / 128 : 1;
   const Cost e = cost_of(epi);
   const float small_pair = (epi == kStats || epi == kDz) && K % 64 != 0 ? kSmallPairOdd : kSmallPair;
   const float large = kLargePair * pairs + e.el, small = small_pair * pairs + e.es;
   const uint32_t full = tp * tl / 256;
-  Timed best = {{(int)tp, 1}, -1.f};
+  Timed best = {{(int)tp, 1, 256}, -1.f};
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
     // all, none, all whole rounds, all but one of them
     if (i > 1 && (tl == 0 || full < i - 2)) continue;
     const uint32_t m = i == 0 ? tp : i == 1 ? 0 : (full - (i - 2)) * 256 / tl;
     const float t = rounds_of(m * tl) * large + rounds_of((tp - m) * ts) * small + (m > 0 && m < tp ? 3000.f : 0.f);
-    if (best.time < 0.f || t < best.time) best = {{(int)m, 1}, t};
+    if (best.time < 0.f || t < best.time) best = {{(int)m, 1, 256}, t};
+  }
+  // Few tokens (w is read once, and that is the time): small tiles that take
+  // fewer rows each, so that all rounds are full.  (Forward in us, D = 3328, V =
+  // 65721 or 257 tiles, 60 tokens: 120 -> 101; V = 151936, 128 tokens of 4096:
+  // 257 -> 233.  For 256 tokens of 1024, V = 20000: 24 -> 25; for 10 of 184, V =
+  // 112369, where the tiles' epilogues count: 26.7 -> 28.0.)
+  if ((epi == kStats || epi == kDz) && few && nq > 0 && nq <= kFewTokens && K >= 512) {
+    const uint32_t most = (tp + 255) / 256 * 256;
+    const int rows = (int)(((uint32_t)np + most - 1) / most + 15) / 16 * 16;
+    best.plan = {0, 1, rows < kLeastRows ? kLeastRows : rows};
   }
   return best;
 }
@@ -1007,7 +1029,7 @@ __host__ __device__ __forceinline__ Timed split_choice(int epi, int i, int np, i
   const float rounds = ceilf((float)tiles * (float)s * (1.f / 256.f));
   const float time = rounds * (i & 1 ? kSmallPair * each + e.es : kLargePair * each + e.el) +
                      (float)s * (float)np * (float)nq * (1.f / 640.f) + (epi == kDw && s > 1 ? 2000.f : 0.f);
-  return {{i & 1 ? 0 : (int)tp, s}, time};
+  return {{i & 1 ? 0 : (int)tp, s, 256}, time};
 }
 // The best of them, found by a wave.
 __device__ __forceinline__ Plan split_plan(int epi, int np, int nq, int K, int most, int lane) {
@@ -1017,7 +1039,7 @@ __device__ __forceinline__ Plan split_plan(int epi, int np, int nq, int K, int m
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) least = fminf(least, __shfl_xor(least, d));
   const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(p.time == least));
-  return Plan{__builtin_amdgcn_readlane(p.plan.large, at), __builtin_amdgcn_readlane(p.plan.splits, at)};
+  return Plan{__builtin_amdgcn_readlane(p.plan.large, at), __builtin_amdgcn_readlane(p.plan.splits, at), 256};
 }
 
 enum { kPlanLogits = 0, kPlanDx = 1, kPlanDw = 2, kPlans = 3 };
@@ -1141,7 +1163,7 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
   if (head) {
     if (threadIdx.x == 0) *o.n = base;
     if (threadIdx.x == 960)
-      o.plans[kPlanLogits] = plan_of(o.top == nullptr ? kStats : kDz, o.piece, base, (int)a.D).plan;
+      o.plans[kPlanLogits] = plan_of(o.top == nullptr ? kStats : kDz, o.piece, base, (int)a.D, o.top != nullptr || a.T <= kFewTokens).plan;
     if (o.top != nullptr) {
       if (wave == 13) {
         const Plan p = split_plan(kDx, base, (int)a.D, o.piece, o.dx_splits, lane);
@@ -1149,7 +1171,7 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
       }
       if (wave == 14) {
         Plan p = split_plan(kDw, (int)a.D, o.piece, base, o.dw_splits, lane);
-        if (p.splits == 1) p = plan_of(kDw, (int)a.D, o.piece, base).plan;
+        if (p.splits == 1) p = plan_of(kDw, (int)a.D, o.piece, base, false).plan;
         if (lane == 0) o.plans[kPlanDw] = p;
       }
       most = wave_max(most);
@@ -1197,7 +1219,7 @@ __global__ __launch_bounds__(NT) void head_join_kernel(const HeadArgs a, const i
   __shared__ float2 got[NT / 64][TT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = threadIdx.x % TT;
   const int64_t t = (int64_t)blockIdx.x * TT + tok;
-  const int parts = plan_at != nullptr ? parts_before((int)((a.V + 255) / 256), plan_at->large) : parts_;
+  const int parts = plan_at != nullptr ? parts_of(a.V, *plan_at) : parts_;
   int p = -1;
   if (t < a.T) p = pos != nullptr ? pos[t] : a.index != nullptr || a.targets[t] >= 0 ? (int)t : -1;
   float top = -INFINITY, sum = 0.f;
@@ -1325,7 +1347,7 @@ __global__ __launch_bounds__(512) void head_finish_kernel(const HeadArgs a, cons
   float q[kEntryLanes], lq[kEntryLanes], z[kEntryLanes];
   int at[kEntryLanes], row[kEntryLanes];
   const bool any = teacher_row(a, t, lane, q, lq, at);
-  const int count = plan_at != nullptr ? parts_before((int)((a.V + 255) / 256), plan_at->large) : parts;
+  const int count = plan_at != nullptr ? parts_of(a.V, *plan_at) : parts;
   const int p = !any ? -1 : pos != nullptr ? pos[t] : (int)t;
   float top = -INFINITY, sum = 0.f;
   auto join = [&](const float2 v) {
@@ -1538,7 +1560,8 @@ struct Forward {
 Forward take_forward(Parts& w, int64_t T, int64_t V, int64_t D) {
   Forward f{};
   if (T > kAsTheyAre) f.c = take_common(w, T, D);
-  f.part = w.take<float2>((V + 255) / 256 * Small::WP * T);
+  // (plan_of's rows of a tile add up to 256 tiles)
+  f.part = w.take<float2>(((V + 255) / 256 + (T <= kFewTokens ? 256 : 0)) * Small::WP * T);
   f.logit = w.take<float>(T);
   f.lse64 = w.take<double>(T);
   return f;
@@ -1730,8 +1753,8 @@ int launch_head(const HeadArgs& a, hipStream_t s) {
     g.plan_at = nullptr;
     MG_RUN(run_tile64<kStats>(g, s));
   } else {
-    g.plan = plan_of(kStats, (int)a.V, (int)a.T, (int)a.D).plan;
-    parts = parts_before(tp, g.plan.large);
+    g.plan = plan_of(kStats, (int)a.V, (int)a.T, (int)a.D, a.T <= kFewTokens).plan;
+    parts = parts_of(a.V, g.plan);
     MG_RUN(run_nt<kStats>(g, s));
   }
   if (a.index != nullptr && a.T < 1024) {

@@ -452,9 +452,11 @@ def test_through_a_layer_and_both_losses():
 
 
 # the weights' gradient in parts over the tokens; the last sizes that go in 64 x
-# 64 tiles and the first that do not; large and small tiles in one product
+# 64 tiles and the first that do not; large and small tiles in one product; few
+# tokens, whose tiles take fewer rows of w than they have
 @pytest.mark.parametrize("T,V,D", [(6000, 700, 200), (3971, 1798, 352), (20000, 130, 72), (64, 16384, 72), (65, 8192, 1544), (65, 16384, 1544),
-                                   (65, 16640, 1544), (1333, 50001, 72), (2050, 3333, 1544), (129, 300, 64), (128, 300, 72)])
+                                   (65, 16640, 1544), (1333, 50001, 72), (2050, 3333, 1544), (129, 300, 64), (128, 300, 72),
+                                   (100, 20011, 1000), (128, 65721, 512), (200, 33333, 264), (256, 66000, 1544), (257, 66000, 72), (127, 70001, 8), (127, 70001, 520)])
 def test_loss_by_every_cut(T, V, D):
     _loss_case(T, V, D, ignored=0.05, z_loss=True, seed=V, uniform=False)
 
