@@ -272,7 +272,7 @@ mg_status mg_head_distill(const void* x, const void* w, const void* teacher, int
                           void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of the workspace of mg_head_loss and mg_head_distill (0 for sizes that
- * they refuse): V T / 8, and for T > 128 2 T D, beside 40 T. */
+ * they refuse): V T / 8, beside 40 T, and for T > 128 2 T D, up to that 8192 T. */
 int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
 
 /* Gradient of mg_head_loss to x and w, from upstream gradients dloss (fp32
@@ -284,9 +284,10 @@ int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
  * do not count) or NULL; dw: bf16 [V, D] (written whole) or NULL: a gradient
  * that is not wanted costs nothing.  z is formed again, a piece of the
  * vocabulary at a time; dz is rounded to bf16 once, relative to the largest of
- * |dloss|, |dloss + dlse| (so that equal weights add no error of their own),
- * the products accumulate in fp32 and are rounded once.  exp(z - lse) has the
- * rounding of lse, 2^-24 |lse| relative, and is 1 at most.  Bitwise reproducible.
+ * |dloss|, |dloss + dlse| (so that equal weights add no error of their own), or,
+ * for T <= 64 and V <= 2^20, taken as the sum of two bf16 values; the products
+ * accumulate in fp32 and are rounded once.  exp(z - lse) has the rounding of lse,
+ * 2^-24 |lse| relative, and is 1 at most.  Bitwise reproducible.
  * workspace: mg_head_bwd_workspace(T, V, D, 0) bytes.  T == 0 writes zero dw. */
 mg_status mg_head_loss_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
                            const float* dloss, const float* dlse, int64_t T, int64_t V, int64_t D,
@@ -304,8 +305,8 @@ mg_status mg_head_distill_bwd(const void* x, const void* w, const void* teacher,
                               void* dw, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of the workspace of the two gradients (k = 0: mg_head_loss_bwd; 0 for
- * sizes that they refuse): 6 T D and at most 1 GiB more for T up to 65536, dz
- * being made for a piece of the vocabulary at a time. */
+ * sizes that they refuse): 6 T D (8 T D for T <= 64) and about 1 GiB at most for
+ * T up to 65536, dz being made for a piece of the vocabulary at a time. */
 int64_t mg_head_bwd_workspace(int64_t T, int64_t V, int64_t D, int32_t k);
 
 /* One group of mgemm_list: D [m, n] = A [m, k] B [n, k]^T (bf16 in and out,

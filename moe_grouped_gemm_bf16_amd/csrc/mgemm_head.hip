@@ -95,7 +95,10 @@ struct Token {
   int32_t target;       // vocabulary entry of w, -1 for none or several (written apart)
 };
 
-enum { kStats = 0, kDz = 1, kDx = 2, kDw = 3 };
+// kDzPair: dz as a sum of two 16-bit values, the second in rows of its own, for
+// few tokens (see kPairs).
+enum { kStats = 0, kDz = 1, kDx = 2, kDw = 3, kDzPair = 4 };
+constexpr bool is_dz(int epi) { return epi == kDz || epi == kDzPair; }
 
 // How a product's tiles are cut, by the number of tokens that count.
 struct Plan {
@@ -375,6 +378,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+__device__ __forceinline__ float low_half(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_half(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
 // Four blocks of 16 x 16 results, 16 bits each, lane l holding of row l % 16
 // and block b columns 4 (l / 16) .. + 3 in x[b], to 16 bytes of one row: out[e]
 // is of row (l % 16 & ~1) + e, block l / 16, columns 8 (l % 2) .. + 7.  So a
@@ -442,7 +448,7 @@ template <int EPI, class C>
 __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const int tp0, const int tp_end,
                                          const int most_splits, const int rows, const int part0, char* lds) {
   constexpr bool kSplit = EPI == kDx || EPI == kDw;
-  constexpr bool kLogits = EPI == kStats || EPI == kDz;
+  constexpr bool kLogits = EPI == kStats || is_dz(EPI);
   constexpr bool kCut = kLogits && C::BQ < 256;       // tiles may take fewer rows of P
   const int own = kCut ? rows : 256;
   const int np = EPI == kDx ? n_tok : a.np;
@@ -581,7 +587,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
       }
     }
 
-    if constexpr (EPI == kDz) {
+    if constexpr (is_dz(EPI)) {
       const bool edge_p = p0 + C::BP > np;
       const float inv = a.top[1];
 #pragma unroll
@@ -604,7 +610,7 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
         const bool told = __builtin_amdgcn_ballot_w64(rel >= 0 && rel < C::BP) != 0;
 #pragma unroll
         for (int i = 0; i < MP; i += 4) {
-          u32x2 pk[4];
+          u32x2 pk[4], low[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float v[4];
@@ -616,6 +622,9 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
             }
             // the one rounding of dz: a 16-bit operand of the two products
             pk[u] = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+            if (EPI == kDzPair)
+              low[u] = u32x2{pack2(v[0] - low_half(pk[u][0]), v[1] - high_half(pk[u][0])),
+                             pack2(v[2] - low_half(pk[u][1]), v[3] - high_half(pk[u][1]))};
           }
           u32x4 out[2];
           regroup(pk, out, lane);
@@ -623,7 +632,17 @@ __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const
           const int pb = pw + p_row(i) + (C::MB == 4 ? 16 * g4 : (g4 >> 1) * (C::BP / 2) + 16 * (g4 & 1));
           char* dz = reinterpret_cast<char*>(a.dz) +
                      ((int64_t)(pb >> 6) * a.rows_t + qw + q_row(j) + (l16 & ~1)) * 128 + 2 * (pb & 63) + 16 * (lane & 1);
-          if (!kCut || pb < p_end) {
+          if constexpr (EPI == kDzPair) {
+            u32x4 rest[2];
+            regroup(low, rest, lane);
+            const int q2 = qw + q_row(j) + (l16 & ~1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (q2 + e < nq && (!kCut || pb < p_end)) {
+                *reinterpret_cast<u32x4*>(dz + 128 * e) = out[e];
+                *reinterpret_cast<u32x4*>(dz + 128 * (nq + e)) = rest[e];
+              }
+          } else if (!kCut || pb < p_end) {
             *reinterpret_cast<u32x4*>(dz) = out[0];
             *reinterpret_cast<u32x4*>(dz + 128) = out[1];
           }
@@ -731,9 +750,9 @@ __device__ __forceinline__ void product(const NtArgs& a, char* lds) {
   if (a.plan_at != nullptr) {
     plan.large = __builtin_amdgcn_readfirstlane(a.plan_at->large);
     plan.splits = __builtin_amdgcn_readfirstlane(a.plan_at->splits);
-    if (EPI == kStats || EPI == kDz) plan.rows = __builtin_amdgcn_readfirstlane(a.plan_at->rows);
+    if (EPI == kStats || is_dz(EPI)) plan.rows = __builtin_amdgcn_readfirstlane(a.plan_at->rows);
   }
-  const int tp = EPI == kStats || EPI == kDz ? (a.np + plan.rows - 1) / plan.rows : ((EPI == kDx ? n : a.np) + 255) / 256;
+  const int tp = EPI == kStats || is_dz(EPI) ? (a.np + plan.rows - 1) / plan.rows : ((EPI == kDx ? n : a.np) + 255) / 256;
   const int large = min(plan.large, tp);
   products<EPI, Large>(a, n, 0, large, plan.splits, plan.rows, 0, lds);
   products<EPI, Small>(a, n, large, tp, plan.splits, plan.rows, parts_before(large, large), lds);
@@ -896,8 +915,16 @@ __global__ __launch_bounds__(512, 2) void tile64_kernel(const NtArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
     char* dz = reinterpret_cast<char*>(a.dz) + ((int64_t)blockIdx.x * a.rows_t + q) * 128 + 2 * (pw - p0);
+    if (EPI == kDzPair && q >= nq) return;
     *reinterpret_cast<u32x2*>(dz) = u32x2{o[0], o[1]};
     *reinterpret_cast<u32x2*>(dz + 16) = u32x2{o[2], o[3]};
+    if (EPI == kDzPair) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e] - low_half(o[e]), v[2 * e + 1] - high_half(o[e]));
+      dz += 128 * (int64_t)nq;
+      *reinterpret_cast<u32x2*>(dz) = u32x2{o[0], o[1]};
+      *reinterpret_cast<u32x2*>(dz + 16) = u32x2{o[2], o[3]};
+    }
   }
 }
 
@@ -1064,6 +1091,7 @@ struct PlaceArgs {
   float* top;                // backward: [2]
   uint16_t* pack;
   int32_t ld, piece, dx_splits, dw_splits;
+  int32_t pair;              // the gradients' products take every token twice
 };
 template <int PER>       // tokens of a thread in a turn, 1024 apart
 __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, const PlaceArgs o) {
@@ -1161,17 +1189,18 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
     base += total;
   }
   if (head) {
-    if (threadIdx.x == 0) *o.n = base;
+    const int rows = o.pair ? 2 * base : base;             // of dz
+    if (threadIdx.x == 0) o.n[0] = base, o.n[1] = rows;
     if (threadIdx.x == 960)
       o.plans[kPlanLogits] = plan_of(o.top == nullptr ? kStats : kDz, o.piece, base, (int)a.D, o.top != nullptr || a.T <= kFewTokens).plan;
     if (o.top != nullptr) {
       if (wave == 13) {
-        const Plan p = split_plan(kDx, base, (int)a.D, o.piece, o.dx_splits, lane);
+        const Plan p = split_plan(kDx, rows, (int)a.D, o.piece, o.dx_splits, lane);
         if (lane == 0) o.plans[kPlanDx] = p;
       }
       if (wave == 14) {
-        Plan p = split_plan(kDw, (int)a.D, o.piece, base, o.dw_splits, lane);
-        if (p.splits == 1) p = plan_of(kDw, (int)a.D, o.piece, base, false).plan;
+        Plan p = split_plan(kDw, (int)a.D, o.piece, rows, o.dw_splits, lane);
+        if (p.splits == 1) p = plan_of(kDw, (int)a.D, o.piece, rows, false).plan;
         if (lane == 0) o.plans[kPlanDw] = p;
       }
       most = wave_max(most);
@@ -1186,12 +1215,16 @@ __global__ __launch_bounds__(1024) void head_place_kernel(const HeadArgs a, cons
       }
     }
   }
-  if (o.pack == nullptr || (base == a.T && o.ld == a.D)) return;
+  if (o.pack == nullptr || (base == a.T && o.ld == a.D && !o.pair)) return;
   __syncthreads();
   for (int i = wave; i * (int64_t)gridDim.x + blockIdx.x < base; i += 16) {
     const u32x4* from = reinterpret_cast<const u32x4*>(a.x + (int64_t)list[i] * a.D);
     u32x4* to = reinterpret_cast<u32x4*>(o.pack + ((int64_t)i * gridDim.x + blockIdx.x) * o.ld);
-    for (int c = lane; c < a.D / 8; c += 64) to[c] = from[c];
+    for (int c = lane; c < a.D / 8; c += 64) {
+      const u32x4 v = from[c];
+      to[c] = v;
+      if (o.pair) to[c + (int64_t)base * o.ld / 8] = v;
+    }
   }
 }
 
@@ -1388,11 +1421,12 @@ __global__ __launch_bounds__(512) void head_finish_kernel(const HeadArgs a, cons
 // Distillation, backward: dz at the entries of a token, from their logits.
 // entry[j]: its place in w (-1: none here, or told by an earlier entry of the
 // same place, whose q then holds both), value[j]: a p - b q, in 16 bits.  With
-// dz (the whole vocabulary's) they are put there at once.
+// dz (the whole vocabulary's) they are put there at once, with `second` what the
+// rounding left as well, *second rows on.
 __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a, const int32_t* pos,
                                                                 const Token* token, const float* top,
                                                                 int32_t* entry, uint16_t* value,
-                                                                int64_t rows_t, uint16_t* dz) {
+                                                                int64_t rows_t, uint16_t* dz, const int32_t* second) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.T) return;
@@ -1423,15 +1457,21 @@ __global__ __launch_bounds__(256) void head_entry_values_kernel(const HeadArgs a
     const int j = 64 * i + lane;
     if (j >= a.k) continue;
     int where = -1;
-    uint32_t bits = 0;
+    uint32_t bits = 0, rest = 0;
     if (any && at[i] >= 0 && !early[i] && at[i] >= a.first && at[i] - a.first < a.V) {
       where = (int)(at[i] - a.first);
       const Token k = token[p];
       const float pr = __builtin_amdgcn_exp2f(below(a.logits_in[t * a.k + j], k.lse) * a.scale);
-      bits = pack2(k.a * top[1] * pr - k.b * top[1] * sum[i], 0.f) & 0xffffu;
+      const float v = k.a * top[1] * pr - k.b * top[1] * sum[i];
+      bits = pack2(v, 0.f) & 0xffffu;
+      rest = pack2(v - low_half(bits), 0.f) & 0xffffu;
     }
     if (dz != nullptr) {
-      if (where >= 0) dz[((int64_t)(where >> 6) * rows_t + p) * 64 + (where & 63)] = (uint16_t)bits;
+      if (where >= 0) {
+        uint16_t* to = dz + ((int64_t)(where >> 6) * rows_t + p) * 64 + (where & 63);
+        *to = (uint16_t)bits;
+        if (second != nullptr) to[64 * (int64_t)*second] = (uint16_t)rest;
+      }
     } else {
       entry[t * a.k + j] = where;
       value[t * a.k + j] = (uint16_t)bits;
@@ -1466,6 +1506,7 @@ struct SumArgs {
   uint16_t* dw;
   int64_t T, V, rows_t;
   int32_t D, pairs;            // pairs of stages of dx's reduction
+  int32_t pair;                // every token's dx is in two rows
   unsigned dx_blocks, dw_blocks;
 };
 __global__ __launch_bounds__(256) void head_sum_kernel(const SumArgs a) {
@@ -1495,6 +1536,12 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const SumArgs a) {
         const float4 lo = f[0], hi = f[1];
         s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
         s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+        if (a.pair && !w) {
+          const float4* g = reinterpret_cast<const float4*>(parts + k * part + (p + *a.n) * a.D + d);
+          const float4 lo2 = g[0], hi2 = g[1];
+          s[0] += lo2.x; s[1] += lo2.y; s[2] += lo2.z; s[3] += lo2.w;
+          s[4] += hi2.x; s[5] += hi2.y; s[6] += hi2.z; s[7] += hi2.w;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = pack2(s[2 * e] * scale, s[2 * e + 1] * scale);
@@ -1534,15 +1581,15 @@ struct Common {
   Token* token;
   uint16_t* xc;
 };
-Common take_common(Parts& w, int64_t T, int64_t D) {
+Common take_common(Parts& w, int64_t T, int64_t D, int64_t rows) {
   Common c;
   c.flag = w.take<uint8_t>(T);
   c.pos = w.take<int32_t>(T);
   c.rows = w.take<int32_t>(T);
-  c.n = w.take<int32_t>(1);
+  c.n = w.take<int32_t>(2);
   c.plans = w.take<Plan>(kPlans);
   c.token = w.take<Token>(T);
-  c.xc = w.take<uint16_t>(T * up(D, 64));
+  c.xc = w.take<uint16_t>(rows * up(D, 64));
   return c;
 }
 
@@ -1559,7 +1606,7 @@ struct Forward {
 
 Forward take_forward(Parts& w, int64_t T, int64_t V, int64_t D) {
   Forward f{};
-  if (T > kAsTheyAre) f.c = take_common(w, T, D);
+  if (T > kAsTheyAre) f.c = take_common(w, T, D, T);
   // (plan_of's rows of a tile add up to 256 tiles)
   f.part = w.take<float2>(((V + 255) / 256 + (T <= kFewTokens ? 256 : 0)) * Small::WP * T);
   f.logit = w.take<float>(T);
@@ -1585,7 +1632,16 @@ struct Backward {
   uint16_t* value;
   int64_t rows_t, piece;
   int32_t dx_splits, dw_splits;
+  bool pair;
 };
+
+// Batches of so few tokens that a tile of the gradients' products has room for
+// each twice take dz as two 16-bit values, the second what the first's rounding
+// left.  With one or two tokens a few of dz's values make up the gradients, and
+// nothing averages their roundings (relative error of dx and dw, 1 or 2 tokens:
+// 0.0025 to 0.0034 with one value, 0.0017 with two, which is the results' own
+// rounding); from some ten tokens on one value gives 0.0019 to 0.0024.
+constexpr int64_t kPairs = 64;
 
 // Most parts of the gradients' reductions: of at least 256 steps each, 256 MiB
 // in all; of dw's only where its tiles are few and the vocabulary one piece.
@@ -1603,9 +1659,10 @@ int32_t dw_splits(int64_t T, int64_t V, int64_t D, int64_t piece) {
 
 Backward take_backward(Parts& w, int64_t T, int64_t V, int64_t D, int64_t k) {
   Backward b{};
-  b.c = take_common(w, T, D);
-  b.rows_t = up(T, 256);
   b.piece = piece_of(T, V);
+  b.pair = T <= kPairs && V <= b.piece;
+  b.c = take_common(w, T, D, b.pair ? 2 * T : T);
+  b.rows_t = up(T, 256);
   b.dx_splits = dx_splits(T, D, b.piece);
   b.dw_splits = dw_splits(T, V, D, b.piece);
   b.top = w.take<float>(2);
@@ -1672,7 +1729,7 @@ int run_tile64(const NtArgs& a, hipStream_t s) {
 
 // Which tokens count, their order and, packed, their rows of x.
 int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t dx_splits, int32_t dw_splits,
-                 float* top, hipStream_t s) {
+                 bool pair, float* top, hipStream_t s) {
   PlaceArgs o{};
   if (a.index != nullptr && a.T > kPlaceFlags) {
     hipLaunchKernelGGL(head_flags_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, c.flag);
@@ -1691,6 +1748,7 @@ int place_tokens(const HeadArgs& a, const Common& c, int64_t piece, int32_t dx_s
   o.piece = (int32_t)piece;
   o.dx_splits = dx_splits;
   o.dw_splits = dw_splits;
+  o.pair = pair;
   const dim3 grid(both ? blocks_for(a.T, 16, 256) : 1);
   if (a.T <= kPlaceFlags) hipLaunchKernelGGL(head_place_kernel<1>, grid, dim3(1024), 0, s, a, o);
   else hipLaunchKernelGGL(head_place_kernel<8>, grid, dim3(1024), 0, s, a, o);
@@ -1741,7 +1799,7 @@ int launch_head(const HeadArgs& a, hipStream_t s) {
   Parts w;
   w.base = static_cast<char*>(a.workspace);
   const Forward f = take_forward(w, a.T, a.V, a.D);
-  if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, 1, nullptr, s));
+  if (f.c.pos != nullptr) MG_RUN(place_tokens(a, f.c, a.V, 1, 1, false, nullptr, s));
   NtArgs g = logits_args(a, f.c, 0, a.V);
   g.targets = f.c.pos != nullptr ? nullptr : a.targets;
   g.part = f.part;
@@ -1788,10 +1846,10 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
   const int32_t T = (int32_t)a.T, D = (int32_t)a.D;
   const int64_t entries = a.index != nullptr ? a.T * a.k : 0;
   const bool one = a.V <= b.piece;
-  MG_RUN(place_tokens(a, b.c, b.piece, b.dx_splits, b.dw_splits, b.top, s));
+  MG_RUN(place_tokens(a, b.c, b.piece, b.dx_splits, b.dw_splits, b.pair, b.top, s));
   auto entry_values = [&](uint16_t* dz) {
     hipLaunchKernelGGL(head_entry_values_kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a, b.c.pos,
-                       b.c.token, b.top, b.entry, b.value, b.rows_t, dz);
+                       b.c.token, b.top, b.entry, b.value, b.rows_t, dz, b.pair ? b.c.n : nullptr);
     return (int)hipGetLastError();
   };
   if (entries > 0 && !one) MG_RUN(entry_values(nullptr));
@@ -1801,8 +1859,9 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     g.top = b.top;
     g.dz = b.dz;
     g.rows_t = b.rows_t;
-    if (tile64(count, T, D)) MG_RUN(run_tile64<kDz>(g, s));
-    else MG_RUN(run_nt<kDz>(g, s));
+    const bool small = tile64(count, T, D);
+    if (b.pair) MG_RUN(small ? run_tile64<kDzPair>(g, s) : run_nt<kDzPair>(g, s));
+    else MG_RUN(small ? run_tile64<kDz>(g, s) : run_nt<kDz>(g, s));
     if (entries > 0 && one) {
       MG_RUN(entry_values(b.dz));
     } else if (entries > 0) {
@@ -1812,7 +1871,7 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     }
     const Operand dz = {b.dz, 128u, (uint32_t)(b.rows_t * 128)};
     NtArgs h{};
-    h.n = b.c.n;
+    h.n = b.c.n + 1;
     h.tokens = T;
     h.D = D;
     h.gq = 4;
@@ -1828,7 +1887,7 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
     x.add = v0 > 0;
     x.dx = a.dx != nullptr ? b.dx32 : nullptr;
     h.P = g.Q;
-    h.x_all = g.x_all;
+    h.x_all = b.pair ? b.c.xc : g.x_all;
     h.Q = dz;
     h.plan_at = b.c.plans + kPlanDw;
     h.np = D;
@@ -1850,6 +1909,7 @@ int launch_head_bwd(const HeadArgs& a, hipStream_t s) {
   o.dw32 = b.dw32;
   o.dx = a.dx;
   o.dw = a.dw;
+  o.pair = b.pair;
   o.T = a.T;
   o.V = a.V;
   o.rows_t = b.rows_t;

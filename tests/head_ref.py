@@ -58,9 +58,10 @@ def forward(x, w, at, q, size, temperature=1.0, first=0):
     return loss, lse, zk, loss_tol, lse_tol, ze[:, None].expand_as(zk)
 
 
-def backward(x, w, at, q, size, lse, up, dense=None, temperature=1.0, first=0):
+def backward(x, w, at, q, size, lse, up, dense=None, temperature=1.0, first=0, step=H):
     """(dx, dw, tolerances of both): up is dloss, dense the weight of the
-    probabilities where it is not dloss."""
+    probabilities where it is not dloss, step dz's rounding: h, or h h where it is
+    the sum of two values (the second is h of dz at most, and rounded to h of it)."""
     X, W, c = x.double(), w.double(), 1.0 / temperature
     T, D = X.shape
     V, k = W.shape[0], at.shape[1]
@@ -79,7 +80,7 @@ def backward(x, w, at, q, size, lse, up, dense=None, temperature=1.0, first=0):
     dz = P - S
     rq = (U * (24 + 8 * size + 2 * k))[:, None]
     dze = P.abs() * (c * ze + U * (16 * A + 16)[:, None]) + S.abs() * rq
-    dze = dze + H * (dz.abs() + dze) + 1e-37
+    dze = dze + step * (dz.abs() + dze) + 1e-37
     dx, dw = dz @ W, dz.T @ X
     m = dz.abs() + dze
     dx_tol = dze @ W.abs() + ((V + 72) * U) * (m @ W.abs())

@@ -132,8 +132,10 @@ def test_workspace_sizes():
     for T, V, D in ((1, 1, 8), (8192, 131072, 4096), (65536, 200000, 2048), (300, 100, 72)):
         fwd, bwd = L.mg_head_workspace(T, V, D), L.mg_head_bwd_workspace(T, V, D, 0)
         wide = -(-D // 64) * 64                       # packed rows of x start on 128 bytes
-        assert 0 < fwd < 2 * T * wide + 40 * T + 16 * T * (V / 128 + 4) + 4096
-        assert 0 < bwd < (1 << 31) + 12 * (T + 256) * D * 64 + (1 << 28) * 2 * D
+        # (up to 128 tokens: up to 256 tiles more, of four parts of 8 bytes; and a
+        # tile of 256 entries more, 256 bytes for each of the parts)
+        assert 0 < fwd < 2 * T * wide + 40 * T + V * T / 8 + (8192 * T if T <= 128 else 0) + 32 * T + 4096
+        assert 0 < bwd < (1 << 30) + 8 * (T + 256) * wide + 40 * T + 4096
         # the entries' places and values are kept where the vocabulary goes in pieces
         assert L.mg_head_bwd_workspace(T, V, D, 64) >= bwd + (6 * 64 * T if T * V > 1 << 28 else 0)
 

@@ -548,3 +548,28 @@ def test_misaligned_tensors_are_refused():
                  lambda: mg.head_loss_bwd(x, w, t, r.lse, r.loss, dx=off)):
         with pytest.raises(mg.MgemmError):
             call()
+
+
+@pytest.mark.parametrize("T,V,D", [(1, 700, 72), (2, 3000, 136), (2, 70001, 520), (17, 2000, 1032), (33, 70001, 264), (64, 3000, 64), (64, 70001, 520)])
+@pytest.mark.parametrize("ignored", [0.0, 0.5])
+def test_few_tokens_keep_dz_in_two_values(T, V, D, ignored):
+    """Up to 64 tokens: only the results' own rounding is left of the bounds."""
+    g, x, w = _inputs(T, V, D, 80 + T)
+    t = _targets(g, T, V, ignored)
+    t[T // 2] = V - 1
+    up = torch.randn(T, device=DEV, generator=g)
+    r = mg.head_loss(x, w, t)
+    e = ref.entries(targets=t)
+    dlse = 0.3 * up
+    dx, dw = mg.head_loss_bwd(x, w, t, r.lse, up, dlse=dlse)
+    wx, ww, tx, tw = ref.backward(x, w, *e, r.lse, up, up.double() + dlse.double(), step=ref.H ** 2)
+    _near("dx", dx, wx, tx)
+    _near("dw", dw, ww, tw)
+    teacher, index = _teacher(g, T, V, 5, torch.float32, ignored)
+    index[T // 2, 0] = 0
+    d = mg.head_distill(x, w, teacher, index, temperature=0.7)
+    e = ref.entries(teacher=teacher, index=index, temperature=0.7)
+    dx, dw = mg.head_distill_bwd(x, w, teacher, index, d.lse, d.logits, up, temperature=0.7)
+    wx, ww, tx, tw = ref.backward(x, w, *e, d.lse, up, temperature=0.7, step=ref.H ** 2)
+    _near("dx", dx, wx, tx)
+    _near("dw", dw, ww, tw)
