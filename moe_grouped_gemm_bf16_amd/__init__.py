@@ -832,6 +832,11 @@ def _teacher(teacher: torch.Tensor, index: torch.Tensor, T: int, temperature: fl
     return k
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous 16-bit tensors share memory."""
+    return a.data_ptr() < b.data_ptr() + 2 * b.numel() and b.data_ptr() < a.data_ptr() + 2 * a.numel()
+
+
 def _head_grads(x, w, dx, dw, need_dx, need_dw, words):
     """The gradients' tensors (None where not wanted) and the workspace."""
     out = []
@@ -847,6 +852,10 @@ def _head_grads(x, w, dx, dw, need_dx, need_dw, words):
                 raise ValueError(f"{name} must be {list(like.shape)}")
         out.append(t)
     _same_device(x.device, dx=out[0], dw=out[1])
+    # the caller's buffers: the weights are still read while gradients are written
+    for name, t, given, others in (("dx", out[0], dx, (x, w)), ("dw", out[1], dw, (x, w, out[0]))):
+        if given is not None and any(o is not None and _overlap(t, o) for o in others):
+            raise ValueError(f"{name} may not overlap x, w or the other gradient")
     return *out, torch.empty(words, dtype=torch.uint8, device=x.device)
 
 

@@ -573,3 +573,17 @@ def test_few_tokens_keep_dz_in_two_values(T, V, D, ignored):
     wx, ww, tx, tw = ref.backward(x, w, *e, d.lse, up, temperature=0.7, step=ref.H ** 2)
     _near("dx", dx, wx, tx)
     _near("dw", dw, ww, tw)
+
+
+def test_buffers_that_overlap_are_refused():
+    T, V, D = 20, 50, 64
+    g, x, w = _inputs(T, V, D, 90)
+    t = _targets(g, T, V, 0.0)
+    r = mg.head_loss(x, w, t)
+    room = torch.empty(T + V, D, dtype=torch.bfloat16, device=DEV)
+    for buffers in (dict(dw=w), dict(dx=x), dict(dx=room[:T], dw=room[T - 1:T - 1 + V])):
+        with pytest.raises(ValueError, match="overlap"):
+            mg.head_loss_bwd(x, w, t, r.lse, r.loss, **buffers)
+    dx, dw = mg.head_loss_bwd(x, w, t, r.lse, r.loss)
+    ox, ow = mg.head_loss_bwd(x, w, t, r.lse, r.loss, dx=room[:T], dw=room[T:])       # side by side
+    assert torch.equal(ox, dx) and torch.equal(ow, dw)
