@@ -241,8 +241,9 @@ mg_status mg_moe_route_bwd(const void* logits, int32_t logits_bf16, const float*
  * logit their sum.  fp32 products and sums of exponentials, in a fixed order:
  * bitwise reproducible.  A NaN or infinite logit makes its token's loss NaN or infinite
  * and no other's; finite ones of any size do neither.
- * D a multiple of 8, 8 <= D <= 2^20; V >= 1 of any size, T <= 2^22; the count of
- * 256 x 128 tiles of z below 2^25, V D below 2^40; 0 <= first, first + V <= 2^31.  x, w 16-byte
+ * D a multiple of 8, 8 <= D <= 2^20; 1 <= V <= 2^31 - 256 of any size (the gradients:
+ * V < 2^31), T <= 2^22; the count of 256 x 128 tiles of z below 2^25, V D below
+ * 2^40; 0 <= first, first + V <= 2^31.  x, w 16-byte
  * aligned, the others 4-byte.  workspace: mg_head_workspace(T, V, D) bytes of
  * DEVICE memory, 16-byte aligned (no contents expected or kept); calls that may
  * run at the same time need one each; no output may overlap an input.  T == 0 is

@@ -514,6 +514,10 @@ bool head_sizes(int64_t T, int64_t V, int64_t D, int64_t k) {
          ((T + 127) / 128) * ((V + 255) / 256) < (int64_t(1) << 25) && V * D < (int64_t(1) << 40);
 }
 
+// The forward takes the vocabulary in one piece and counts its tiles of 256 rows in
+// 32 bits, the last one rounded up (the gradients' pieces are far shorter).
+constexpr int64_t kMaxVocabulary = kMaxRows - 255;
+
 // Checks that the four calls share; k == 0: a target per token, `index` holds them.
 mg_status check_head(const mg::HeadArgs& a, const int32_t* index, int64_t k, int64_t need,
                      int64_t workspace_bytes) {
@@ -533,6 +537,7 @@ mg_status check_head(const mg::HeadArgs& a, const int32_t* index, int64_t k, int
 mg_status head_forward(mg::HeadArgs& a, const int32_t* index, int64_t k, float* loss, float* lse,
                        float* logits, void* workspace, int64_t workspace_bytes, void* stream) {
   a.workspace = workspace;
+  if (a.V > kMaxVocabulary) return MG_ERR_SHAPE;
   mg_status st = check_head(a, index, k, mg_head_workspace(a.T, a.V, a.D), workspace_bytes);
   if (st != MG_OK) return st;
   if (a.T == 0) return MG_OK;
@@ -599,7 +604,7 @@ mg::HeadArgs distill_args(const void* x, const void* w, const void* teacher, int
 }  // namespace
 
 int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D) {
-  return head_sizes(T, V, D, 0) && T > 0 ? mg::head_workspace_bytes(T, V, D) : 0;
+  return head_sizes(T, V, D, 0) && V <= kMaxVocabulary && T > 0 ? mg::head_workspace_bytes(T, V, D) : 0;
 }
 
 int64_t mg_head_bwd_workspace(int64_t T, int64_t V, int64_t D, int32_t k) {
