@@ -288,7 +288,8 @@ int64_t mg_head_workspace(int64_t T, int64_t V, int64_t D);
  * |dloss|, |dloss + dlse| (so that equal weights add no error of their own), or,
  * for T <= 64 and V <= 2^20, taken as the sum of two bf16 values; the products
  * accumulate in fp32 and are rounded once.  exp(z - lse) has the rounding of lse,
- * 2^-24 |lse| relative, and is 1 at most.  Bitwise reproducible.
+ * 2^-24 |lse| relative (mg_head_distill_bwd at a temperature other than 1 rounds
+ * lse / c as well: 2^-23 |lse|), and is 1 at most.  Bitwise reproducible.
  * workspace: mg_head_bwd_workspace(T, V, D, 0) bytes.  T == 0 writes zero dw. */
 mg_status mg_head_loss_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
                            const float* dloss, const float* dlse, int64_t T, int64_t V, int64_t D,
