@@ -523,8 +523,8 @@ mg_status check_head(const mg::HeadArgs& a, const int32_t* index, int64_t k, int
                      int64_t workspace_bytes) {
   if (!head_sizes(a.T, a.V, a.D, k) || a.first < 0 || a.first > kMaxRows + 1 - a.V)
     return MG_ERR_SHAPE;
-  // (no NaN; a factor that is a normal number)
-  if (!(a.c >= 1e-37 && a.c <= 1e37)) return MG_ERR_SHAPE;
+  // temperatures of 1e-37 to 1e37 as fp32 has them (no NaN; a factor that is a normal number)
+  if (!(a.c >= 1.0 / 1e37f && a.c <= 1.0 / 1e-37f)) return MG_ERR_SHAPE;
   if (a.T == 0) return MG_OK;
   if (workspace_bytes < need) return MG_ERR_SHAPE;
   if (!a.x || !a.w || !index || (k > 0 && !a.teacher) || !a.workspace) return MG_ERR_NULL;

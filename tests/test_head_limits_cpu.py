@@ -26,3 +26,14 @@ def test_the_longest_vocabulary_has_a_workspace():
     assert L.mg_head_workspace(1, V, 8) >= V // 256 * 4 * 8
     # the gradients take it in pieces and have no such end
     assert L.mg_head_bwd_workspace(1, (1 << 31) - 1, 8, 0) > 0
+
+
+def test_both_ends_of_the_temperature_are_taken():
+    # (no tokens: nothing to launch)
+    import numpy as np
+    low, high = np.float32(1e-37), np.float32(1e37)
+    for tau, status in ((low, 0), (high, 0), (np.nextafter(low, np.float32(0)), SHAPE),
+                        (np.nextafter(high, np.float32(np.inf)), SHAPE)):
+        tau = float(tau)
+        assert L.mg_head_distill(A, A, A, 0, A, 0, 9, 16, 3, 0, tau, A, A, A, A, 0, None) == status, tau
+        assert L.mg_head_distill_bwd(A, A, A, 0, A, A, A, A, 0, 9, 16, 3, 0, tau, A, None, A, 0, None) == status, tau
