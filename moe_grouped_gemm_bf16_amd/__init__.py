@@ -862,7 +862,8 @@ def _head_grads(x, w, dx, dw, need_dx, need_dw, words):
 def head_loss(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, first: int = 0) -> HeadLoss:
     """Cross entropy of the output head, without keeping the logits z = x w^T.
 
-    x bf16 [T, D], w bf16 [V, D] (D a multiple of 8, any V), targets int32 [T].
+    x bf16 [T, D], w bf16 [V, D] (D a multiple of 8, V of any size up to
+    2^31 - 256), targets int32 [T].
     loss = lse - logit per token, lse = logsumexp(z), logit = z[target].  A
     token with a negative target does not count: its loss, lse and logit are 0.
     Where the vocabulary is spread over ranks, `first` is the index of w's row

@@ -301,9 +301,8 @@ struct Core {
   __device__ __forceinline__ void loadQ() const { Q.template load<HALF, BUF>(live, left, wave); }
 
   // 16 x 16 x 32 products: an accumulator is read and written once in 32 steps.
-  // (32 x 32 x 16 ones, once in 16, drew so much more power that the chip ran at
-  // 1.60 GHz, not 1.70, and kept the matrix cores 75% busy: 8192 x 131072 x 2048
-  // with the forward's epilogue 1275 TFLOP/s, with these 1404.)
+  // (With 32 x 32 x 16 ones, once in 16, the chip drew more power and ran at 1.60
+  // GHz, not 1.70: loss of 8192 x 131072 x 4096 in 6.68 ms, with these 6.38.)
   template <int HP, int HQ>
   __device__ __forceinline__ void mul(const bf16x8 (&A)[C::MB][2], const bf16x8 (&B)[2][2]) {
 #pragma unroll
@@ -449,8 +448,12 @@ __device__ __forceinline__ Item item_of(int id, int tp, int tq, int gq) {
 // XCD has a contiguous range of tiles, gq of them along Q at a time, that
 // share operand rows in its L2.  Bound by the matrix cores (busy 67% to 72% of
 // the cycles) and by the clock that their power leaves (1.7 to 1.8 GHz): 8192
-// tokens, V = 131072, D = 4096, forward 6.05 to 6.28 ms, 1400 to 1455 TFLOP/s
-// (the product alone by the library: 1503); backward 19.5 to 19.9 ms, 1325 to 1355.
+// tokens, V = 131072, D = 4096, forward 6.0 to 6.5 ms on different cards, 1350 to
+// 1460 TFLOP/s (the product alone by the library: 1503); backward 19.4 to 20.5,
+// 1290 to 1360.
+// The weight gradient's loop on 256 x 256 tiles has more values than registers: three
+// are read back from scratch in every pair of stages, and such a read waits for the
+// loads in flight as well.
 template <int EPI, class C>
 __device__ __forceinline__ void products(const NtArgs& a, const int n_tok, const int tp0, const int tp_end,
                                          const int most_splits, const int rows, const int part0, char* lds) {
@@ -1043,9 +1046,9 @@ __host__ __device__ __forceinline__ Timed plan_of(int epi, int np, int nq, int K
     if (best.time < 0.f || t < best.time) best = {{(int)m, 1, 256}, t};
   }
   // Few tokens (w is read once, and that is the time): small tiles that take
-  // fewer rows each, so that all rounds are full.  (Forward in us, D = 3328, V =
-  // 65721 or 257 tiles, 60 tokens: 120 -> 101; V = 151936, 128 tokens of 4096:
-  // 257 -> 233.  For 256 tokens of 1024, V = 20000: 24 -> 25; for 10 of 184, V =
+  // fewer rows each, so that all rounds are full.  (The forward's kernel in us, D =
+  // 3328, V = 65721 or 257 tiles, 60 tokens: 120 -> 101; V = 151936, 128 tokens of
+  // 4096: 257 -> 233.  For 256 tokens of 1024, V = 20000: 24 -> 25; for 10 of 184, V =
   // 112369, where the tiles' epilogues count: 26.7 -> 28.0.)
   if ((epi == kStats || epi == kDz) && few && nq > 0 && nq <= kFewTokens && K >= 512) {
     const uint32_t most = (tp + 255) / 256 * 256;
@@ -1652,7 +1655,8 @@ struct Backward {
 // left.  With one or two tokens a few of dz's values make up the gradients, and
 // nothing averages their roundings (relative error of dx and dw, 1 or 2 tokens:
 // 0.0025 to 0.0034 with one value, 0.0017 with two, which is the results' own
-// rounding); from some ten tokens on one value gives 0.0019 to 0.0024.
+// rounding); from some ten tokens on one value gives 0.0019 to 0.0024.  It costs
+// stores and products: 14 x 90642 x 3312 477 -> 494 us.
 constexpr int64_t kPairs = 64;
 
 // Most parts of the gradients' reductions: of at least 256 steps each, 256 MiB
